@@ -126,12 +126,16 @@ def _layout(c, device):
     def place(lane, half, byte):
         return ((byte // piece) * 2 + half) * 32 * piece + lane * piece + byte % piece
 
-    t, bit = j // (gs // 4), (g * (gs // 4) + j % (gs // 4)) * b
+    # K: the channels 2i and 2i + 1 of a 32-bit word's codes are at fields i and i + half of the fields (bytes: in order)
+    t, slot, per = j // (gs // 4), g * (gs // 4) + j % (gs // 4), 32 // b
+    field = slot if b == 8 else slot // per * per + slot % per // 2 + slot % 2 * (per // 2)
+    bit = field * b
     k_at = place((tok % 8)[:, None] * 4 + t, (tok // 8)[:, None], bit // 8)
+    k_order = (t * hd + field).argsort().view(-1, 8 // b)
     u, slot = j // (gs // 8), g * (gs // 8) + j % (gs // 8)
     unit, rest = slot // (16 // b), slot % (16 // b) * b
     v_at = place(u * 4 + (tok % 8)[:, None] // 2, (tok // 8)[:, None], unit * 4 + (tok % 2)[:, None] * 2 + rest // 8)
-    return {"k": (k_at, bit % 8, (t * hd + bit // b).argsort().view(-1, 8 // b)),
+    return {"k": (k_at, bit % 8, k_order),
             "v": (v_at, rest % 8, (u * hd + slot).argsort().view(-1, 8 // b))}
 
 
@@ -418,6 +422,8 @@ def _exact_cache(c, s, b, length):
             q = torch.where(e > 0, (8 + m) * torch.exp2(e.double() - 10), m * 2.0 ** -9) * (1.0 - 2.0 * (byte >> 7))
         else:
             q = torch.stack([(lanes.long() // 2 ** (bits * i)) % 2 ** bits for i in range(8 // bits)], -1).flatten(-2).double()
+        if which == 0 and bits < 8:  # a word's even channels come before its odd ones
+            q = q.unflatten(-1, (-1, 2, 16 // bits)).transpose(-1, -2).flatten(-3)
         q = q.reshape(blocks, hkv, 16, q.shape[-2], ng, -1).transpose(3, 4).reshape(blocks, hkv, 16, ng, gs)
         sz = part[..., 16 * hd * bits // 8:].contiguous().view(torch.float16).double().reshape(blocks, hkv, 16, ng, 2)
         v = (q - sz[..., 1:]) * sz[..., :1]
