@@ -115,6 +115,8 @@ typedef enum ttq_qscheme {
 #define TTQ_FLAG_RANK_DEFICIENT 0x10u /* ttq_lowrank_init: W's sampled range had fewer than
                                          r + oversample independent directions (a Cholesky
                                          pivot was not positive and was floored) */
+#define TTQ_FLAG_BAD_INDEX 0x20u /* ttq_kv_*: a sequence's rows or length, or a page number, out of
+                                    range (what it names was skipped) */
 
 /* Byte offsets of the workspace regions for one problem shape (all 256-byte
  * aligned); `total` equals ttq_workspace_size(...).  After
@@ -427,7 +429,8 @@ ttq_status ttq_get_status(const void* ws, uint32_t* flags);
  * value, a binary16 scale overflow, an activation beyond binary16, or a bit
  * this version does not define); else TTQ_OK.  TTQ_FLAG_RANK_DEFICIENT is a
  * warning: a weight of rank below r + oversample is a valid input to
- * ttq_lowrank_init, whose outputs stay finite. */
+ * ttq_lowrank_init, whose outputs stay finite.  TTQ_FLAG_BAD_INDEX alone
+ * (or with that warning) is TTQ_ERR_INVALID_ARG. */
 ttq_status ttq_status_from_flags(uint32_t flags);
 
 /* ---------------------------------------------------------------------

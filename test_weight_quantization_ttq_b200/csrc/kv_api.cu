@@ -1,0 +1,201 @@
+// The C ABI of the quantised key/value cache (declared in include/ttq_kv.h):
+// argument checks and launches.  Nothing here allocates device memory or
+// synchronises.
+#include <cmath>
+
+#include "kv_attention.cuh"
+#include "ttq_kv.h"
+
+namespace ttq {
+namespace {
+
+constexpr size_t kStatusBytes = 4096;     // the least workspace an entry point takes
+constexpr size_t kKvHeader = 4096;        // the attention's regions start here
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return kKvPlanSMs;
+  return n;
+}
+
+bool format_built(int hd, int bits, int group) {
+  if (hd != 64 && hd != 128 && hd != 256) return false;
+  if (bits != 2 && bits != 4 && bits != 8) return false;
+  if (group != 32 && group != 64 && group != 128 && group != 256) return false;
+  return group <= hd && hd / group <= 4;
+}
+
+size_t page_bytes(int page_size, int kv_heads, int hd, int bits, int group) {
+  if (page_size < 16 || page_size > 65536 || page_size % 16 != 0 || kv_heads < 1 || kv_heads > 65535) return 0;
+  if (!format_built(hd, bits, group)) return 0;
+  return static_cast<size_t>(kv_heads) * (page_size / 16) * kv_block_bytes(hd, bits, group);
+}
+
+// The checks that the three entry points share, and the kernels' view.
+ttq_status geometry(const ttq_kv_cache* c, const ttq_kv_batch* b, void* ws, size_t ws_bytes, KvGeometry* g) {
+  if (c == nullptr || b == nullptr) return TTQ_ERR_INVALID_ARG;
+  if (c->scheme != TTQ_QSCHEME_ASYMMETRIC && c->scheme != TTQ_QSCHEME_SYMMETRIC && c->scheme != TTQ_QSCHEME_FP8_E4M3)
+    return TTQ_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16 != 0) return TTQ_ERR_INVALID_ARG;
+  if (c->kv_heads < 1 || c->kv_heads > 65535 || c->num_pages < 0 || c->num_pages > INT32_MAX) return TTQ_ERR_INVALID_ARG;
+  if (!format_built(c->head_dim, c->bits, c->group)) return TTQ_ERR_UNSUPPORTED;
+  if ((c->bits == 8) != (c->scheme == TTQ_QSCHEME_FP8_E4M3)) return TTQ_ERR_UNSUPPORTED;
+  if (b->batch < 0 || b->rows < 0 || b->max_new < 0 || b->table_stride < 0) return TTQ_ERR_INVALID_ARG;
+  if (b->rows > INT32_MAX || b->table_stride > INT32_MAX) return TTQ_ERR_INVALID_ARG;
+  if (b->batch > kKvMaxBatch) return TTQ_ERR_UNSUPPORTED;
+  if (b->batch > 0 && (b->kv_len == nullptr || b->cu_new == nullptr)) return TTQ_ERR_INVALID_ARG;
+  if (b->batch > 0 && b->table_stride > 0 && b->page_table == nullptr) return TTQ_ERR_INVALID_ARG;
+  if (c->num_pages > 0 && c->pages == nullptr) return TTQ_ERR_INVALID_ARG;
+  if (!aligned(c->pages, 16) || !aligned(b->page_table, 4) || !aligned(b->kv_len, 4) || !aligned(b->cu_new, 4))
+    return TTQ_ERR_INVALID_ARG;
+  for (const float* d : {c->D_k, c->D_v, c->D_k_rsqrt, c->D_v_rsqrt})
+    if (!aligned(d, 16)) return TTQ_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned(ws, 256)) return TTQ_ERR_INVALID_ARG;
+  if (ws_bytes < kStatusBytes) return TTQ_ERR_WORKSPACE;
+  g->pages = static_cast<uint8_t*>(c->pages);
+  g->num_pages = c->num_pages;
+  g->page_bytes = static_cast<int64_t>(page_bytes(c->page_size, c->kv_heads, c->head_dim, c->bits, c->group));
+  g->page_blocks = c->page_size / 16;
+  g->kv_heads = c->kv_heads;
+  g->table = b->page_table;
+  g->table_stride = b->table_stride;
+  g->kv_len = b->kv_len;
+  g->cu = b->cu_new;
+  g->batch = static_cast<int>(b->batch);
+  g->rows = b->rows;
+  g->max_new = static_cast<int>(b->max_new < INT32_MAX ? b->max_new : INT32_MAX);
+  g->status = static_cast<uint32_t*>(ws);
+  return TTQ_OK;
+}
+
+bool row_type(ttq_dtype t) { return t == TTQ_F32 || t == TTQ_BF16 || t == TTQ_F16; }
+
+// Rows with the given strides: 16-byte loads of 8 channels.
+bool strides_ok(const void* p, int64_t row, int64_t head) {
+  return aligned(p, 16) && row >= 0 && head >= 0 && row % 8 == 0 && head % 8 == 0;
+}
+
+ttq_status status_of(cudaError_t e) { return e == cudaSuccess ? TTQ_OK : TTQ_ERR_CUDA; }
+
+}  // namespace
+
+// 8, 16 or 32 query rows per tile: the fewest that hold a sequence's rows of
+// one key/value head, since rows of a tile that are not there cost as much as
+// those that are, while every further tile reads and unpacks the codes again.
+// Heads of 256 channels stop at 16 (their accumulators fill the registers).
+KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows) {
+  KvAttentionPlan p = {};
+  if (!format_built(hd, bits, group)) return p;
+  p.nt = tile_rows <= 8 ? 1 : (tile_rows <= 16 || hd == 256) ? 2 : 4;
+  const int ctas = hd == 64    ? kv_attention_ctas_hd64(bits, group, p.nt)
+                   : hd == 128 ? kv_attention_ctas_hd128(bits, group, p.nt)
+                               : kv_attention_ctas_hd256(bits, group, p.nt);
+  p.grid = ctas * kKvPlanSMs;
+  p.slot_floats = static_cast<int64_t>(8 * p.nt) * (hd + 2);
+  p.meta_bytes = static_cast<int64_t>(p.grid) * 2 * sizeof(int4);
+  p.part_bytes = 2 * p.grid * p.slot_floats * 4;
+  return p;
+}
+
+cudaError_t launch_kv_attention(const KvAttentionArgs& a, int hd, int bits, int group,
+                                const KvAttentionPlan& plan, cudaStream_t stream) {
+  if (hd == 64) return kv_attention_hd64(a, bits, group, plan, stream);
+  if (hd == 128) return kv_attention_hd128(a, bits, group, plan, stream);
+  return kv_attention_hd256(a, bits, group, plan, stream);
+}
+
+}  // namespace ttq
+
+extern "C" {
+
+using namespace ttq;
+
+size_t ttq_kv_page_bytes(int page_size, int kv_heads, int head_dim, int bits, int group) {
+  return page_bytes(page_size, kv_heads, head_dim, bits, group);
+}
+
+ttq_status ttq_kv_write(const ttq_kv_cache* cache, const ttq_kv_batch* batch, const void* K,
+                        int64_t k_row, int64_t k_head, const void* V, int64_t v_row,
+                        int64_t v_head, ttq_dtype dtype, void* ws, size_t ws_bytes, void* stream) {
+  KvWriteArgs a;
+  const ttq_status st = geometry(cache, batch, ws, ws_bytes, &a.g);
+  if (st != TTQ_OK) return st;
+  if (!row_type(dtype)) return TTQ_ERR_INVALID_ARG;
+  if (!strides_ok(K, k_row, k_head) || !strides_ok(V, v_row, v_head)) return TTQ_ERR_INVALID_ARG;
+  if (batch->rows == 0 || batch->batch == 0) return TTQ_OK;
+  if (K == nullptr || V == nullptr) return TTQ_ERR_INVALID_ARG;
+  a.x[0] = K, a.x[1] = V;
+  a.row[0] = k_row, a.row[1] = v_row;
+  a.head[0] = k_head, a.head[1] = v_head;
+  a.D[0] = cache->D_k, a.D[1] = cache->D_v;
+  return status_of(launch_kv_write(a, cache->head_dim, cache->bits, cache->group,
+                                   cache->scheme == TTQ_QSCHEME_SYMMETRIC, dtype, sms(),
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+ttq_status ttq_kv_read(const ttq_kv_cache* cache, const ttq_kv_batch* batch, void* K, void* V,
+                       ttq_dtype dtype, void* ws, size_t ws_bytes, void* stream) {
+  KvReadArgs a;
+  const ttq_status st = geometry(cache, batch, ws, ws_bytes, &a.g);
+  if (st != TTQ_OK) return st;
+  if (!row_type(dtype) || !aligned(K, 16) || !aligned(V, 16)) return TTQ_ERR_INVALID_ARG;
+  if (batch->rows == 0 || batch->batch == 0 || (K == nullptr && V == nullptr)) return TTQ_OK;
+  a.y[0] = K, a.y[1] = V;
+  a.Dr[0] = cache->D_k_rsqrt, a.Dr[1] = cache->D_v_rsqrt;
+  return status_of(launch_kv_read(a, cache->head_dim, cache->bits, cache->group, dtype, sms(),
+                                  static_cast<cudaStream_t>(stream)));
+}
+
+size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_t heads,
+                                       int64_t kv_heads, int64_t max_new) {
+  if (kv_heads < 1 || heads < kv_heads || heads % kv_heads != 0 || heads > 65535) return 0;
+  if (max_new < 0 || max_new > kKvMaxNew) return 0;
+  const KvAttentionPlan p = kv_attention_plan(head_dim, bits, group, max_new * (heads / kv_heads));
+  if (p.grid == 0) return 0;
+  return kKvHeader + p.meta_bytes + p.part_bytes;
+}
+
+ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch, const void* Q,
+                            int64_t q_row, int64_t q_head, ttq_dtype dtype, int64_t heads,
+                            float scale, float softcap, int64_t window, const uint64_t* tree,
+                            void* Y, ttq_dtype y_dtype, void* ws, size_t ws_bytes, void* stream) {
+  KvAttentionArgs a;
+  const ttq_status st = geometry(cache, batch, ws, ws_bytes, &a.g);
+  if (st != TTQ_OK) return st;
+  if (!row_type(dtype) || !row_type(y_dtype)) return TTQ_ERR_INVALID_ARG;
+  if (heads < 1 || heads > 65535 || heads % cache->kv_heads != 0) return TTQ_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return TTQ_ERR_INVALID_ARG;
+  if (!strides_ok(Q, q_row, q_head) || !aligned(Y, 16) || !aligned(tree, 8)) return TTQ_ERR_INVALID_ARG;
+  if (batch->max_new > kKvMaxNew) return TTQ_ERR_UNSUPPORTED;
+  const size_t need = ttq_kv_attention_workspace_size(cache->head_dim, cache->bits, cache->group, heads,
+                                                      cache->kv_heads, batch->max_new);
+  if (ws_bytes < need) return TTQ_ERR_WORKSPACE;
+  if (batch->rows == 0 || batch->batch == 0 || batch->max_new == 0) return TTQ_OK;
+  if (Q == nullptr || Y == nullptr) return TTQ_ERR_INVALID_ARG;
+  const int per = static_cast<int>(heads / cache->kv_heads);
+  const KvAttentionPlan p = kv_attention_plan(cache->head_dim, cache->bits, cache->group, batch->max_new * per);
+  a.Dk = cache->D_k_rsqrt;
+  a.Dv = cache->D_v_rsqrt;
+  a.Q = Q;
+  a.q_row = q_row;
+  a.q_head = q_head;
+  a.q_type = dtype;
+  a.y_type = y_dtype;
+  a.heads = static_cast<int>(heads);
+  a.per = per;
+  a.scale = scale;
+  a.cap = softcap;
+  a.window = window;
+  a.tree = tree;
+  a.Y = Y;
+  a.meta = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kKvHeader);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kKvHeader + p.meta_bytes);
+  return status_of(launch_kv_attention(a, cache->head_dim, cache->bits, cache->group, p,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,12 @@
+// Attention over the quantised cache: head size 128 (kv_attention.cuh).
+#include "kv_attention.cuh"
+
+namespace ttq {
+
+cudaError_t kv_attention_hd128(const KvAttentionArgs& a, int bits, int group, const KvAttentionPlan& p,
+                              cudaStream_t stream) {
+  return kv_attention_launch<128>(a, bits, group, p, stream);
+}
+int kv_attention_ctas_hd128(int bits, int group, int nt) { return kv_attention_ctas<128>(bits, group, nt); }
+
+}  // namespace ttq

@@ -1,0 +1,12 @@
+// Attention over the quantised cache: head size 256 (kv_attention.cuh).
+#include "kv_attention.cuh"
+
+namespace ttq {
+
+cudaError_t kv_attention_hd256(const KvAttentionArgs& a, int bits, int group, const KvAttentionPlan& p,
+                              cudaStream_t stream) {
+  return kv_attention_launch<256>(a, bits, group, p, stream);
+}
+int kv_attention_ctas_hd256(int bits, int group, int nt) { return kv_attention_ctas<256>(bits, group, nt); }
+
+}  // namespace ttq

@@ -1,0 +1,155 @@
+// Device-side helpers of the key/value cache's kernels: where a token's
+// codes are in a block, and where a row of the batch is in the cache.
+//
+// A block holds 16 tokens of one head as K codes, K (scale, zero) pairs, V
+// codes, V pairs.  The codes stand as the lanes of a warp take them for the
+// A operand of m16n8k16: lane 4 a + c of a K block has, of tokens a and
+// a + 8 (its two halves), the channels r in [c g / 4, (c + 1) g / 4) of
+// every group of g; lane 4 a + c of a V block has, of the channels r in
+// [a g / 8, (a + 1) g / 8) of every group, the tokens 2 c, 2 c + 1 and 2 c + 8,
+// 2 c + 9.  A lane's bytes of one half are cut into pieces of at most 16 bytes,
+// and a piece of all lanes is contiguous, so that a warp reads it without
+// bank conflicts.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include <cstring>
+
+#include "kv_kernels.h"
+#include "ttq_device.cuh"
+
+namespace ttq {
+
+template <int HD, int BITS, int NG>
+struct KvFormat {
+  static constexpr int G = HD / NG;                     // channels of a group
+  static constexpr int LB = HD * BITS / 32;             // a lane's bytes of one half
+  static constexpr int PIECE = LB < 16 ? LB : 16;
+  static constexpr int CODES = kv_code_bytes(HD, BITS);
+  static constexpr int PAIRS = kv_pair_bytes(HD, G);
+  static constexpr int BLOCK = 2 * (CODES + PAIRS);
+  static constexpr int V_OFFSET = CODES + PAIRS;        // the V part within the block
+  static_assert(BLOCK % 16 == 0, "a block is one bulk copy");
+
+  static __device__ __forceinline__ int place(int lane, int half, int byte) {
+    return ((byte / PIECE) * 2 + half) * 32 * PIECE + lane * PIECE + byte % PIECE;
+  }
+};
+
+// Where the rows of the batch are.  Sequence b is valid when its rows lie in
+// [0, rows), are at most max_new and kv_len, and kv_len fits its table.
+struct KvSequence {
+  int row0, n, kv;
+};
+__device__ __forceinline__ bool kv_sequence(const KvGeometry& g, int b, KvSequence& s) {
+  const int c0 = g.cu[b], c1 = g.cu[b + 1];
+  const int kv = g.kv_len[b];
+  s.row0 = c0;
+  s.n = c1 - c0;
+  s.kv = kv;
+  return c0 >= 0 && c1 >= c0 && c1 <= g.rows && c1 - c0 <= g.max_new && kv >= c1 - c0 &&
+         kv <= g.table_stride * g.page_blocks * 16;
+}
+
+// The sequence that holds row r, or -1: the last b with cu[b] <= r, when
+// r < cu[b + 1].
+__device__ __forceinline__ int kv_find_sequence(const KvGeometry& g, int64_t r) {
+  int lo = 0, hi = g.batch;          // cu[lo] <= r < cu[hi] once the ends are checked
+  if (g.batch == 0 || g.cu[0] > r || g.cu[g.batch] <= r) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (g.cu[mid] <= r) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// The block of position p of a sequence in the cache, for head h; null when
+// its page is not one of the cache's.
+__device__ __forceinline__ uint8_t* kv_block(const KvGeometry& g, int b, int p, int h, int block_bytes) {
+  const int blk = p >> 4;
+  const int page = g.table[b * g.table_stride + blk / g.page_blocks];
+  if (page < 0 || page >= g.num_pages) return nullptr;
+  return g.pages + page * g.page_bytes +
+         (static_cast<int64_t>(h) * g.page_blocks + blk % g.page_blocks) * block_bytes;
+}
+
+__device__ __forceinline__ uint32_t h2_as_u32(__half2 v) {
+  uint32_t u;
+  memcpy(&u, &v, 4);
+  return u;
+}
+__device__ __forceinline__ __half2 u32_as_h2(uint32_t u) {
+  __half2 v;
+  memcpy(&v, &u, 4);
+  return v;
+}
+
+// Two E4M3 codes (low 16 bits) as a binary16 pair: exact.
+__device__ __forceinline__ uint32_t kv_e4m3x2(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+// NaN-keeping minimum and maximum.
+__device__ __forceinline__ float kv_min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float kv_max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 8 consecutive elements of a row as float32, and back (rounded to nearest
+// even); all addresses are 16-byte aligned.
+template <int TYPE>
+__device__ __forceinline__ void kv_load8(const void* p, int64_t at, float (&x)[8]) {
+  if constexpr (TYPE == kRowF32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 a = s[0], b = s[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TYPE == kRowBF16) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(u32_as_h2(w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t kv_pack2(float a, float b) {
+  if constexpr (TYPE == kRowBF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    uint32_t u;
+    memcpy(&u, &v, 4);
+    return u;
+  } else {
+    return h2_as_u32(__floats2half2_rn(a, b));
+  }
+}
+template <int TYPE>
+__device__ __forceinline__ void kv_store8(void* p, int64_t at, const float (&x)[8]) {
+  if constexpr (TYPE == kRowF32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+    d[0] = make_float4(x[0], x[1], x[2], x[3]);
+    d[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
+        make_uint4(kv_pack2<TYPE>(x[0], x[1]), kv_pack2<TYPE>(x[2], x[3]), kv_pack2<TYPE>(x[4], x[5]),
+                   kv_pack2<TYPE>(x[6], x[7]));
+  }
+}
+
+}  // namespace ttq

@@ -1,0 +1,87 @@
+// Host-side launchers of the key/value cache's kernels (internal to
+// libttq.so) and what they share.  Argument checking is done by the C ABI
+// layer (kv_api.cu) before these are called.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ttq {
+
+constexpr int kKvMaxBatch = 1024;
+constexpr int kKvMaxNew = 64;
+constexpr int kKvPlanSMs = 148;   // fixed so that workspace sizes are device-independent
+
+// Element types of the row tensors (the values of ttq_dtype).
+constexpr int kRowF32 = 0;
+constexpr int kRowBF16 = 1;
+constexpr int kRowF16 = 2;
+
+// Bytes of one part of a block of 16 tokens of one head.
+constexpr int kv_code_bytes(int hd, int bits) { return 16 * hd * bits / 8; }
+constexpr int kv_pair_bytes(int hd, int group) { return 16 * (hd / group) * 4; }
+constexpr int kv_block_bytes(int hd, int bits, int group) {
+  return 2 * (kv_code_bytes(hd, bits) + kv_pair_bytes(hd, group));
+}
+
+// The cache and the batch as the kernels take them.
+struct KvGeometry {
+  uint8_t* pages = nullptr;
+  int64_t num_pages = 0, page_bytes = 0;
+  int page_blocks = 1;          // blocks of 16 tokens in a page
+  int kv_heads = 1;
+  const int32_t* table = nullptr;
+  int64_t table_stride = 0;
+  const int32_t* kv_len = nullptr;
+  const int32_t* cu = nullptr;
+  int batch = 0;
+  int64_t rows = 0;
+  int max_new = 0;
+  uint32_t* status = nullptr;
+};
+
+struct KvWriteArgs {
+  KvGeometry g;
+  const void* x[2] = {};        // K, V rows
+  int64_t row[2] = {}, head[2] = {};
+  const float* D[2] = {};
+};
+cudaError_t launch_kv_write(const KvWriteArgs& a, int hd, int bits, int group, bool symmetric,
+                            int dtype, int num_sms, cudaStream_t stream);
+
+struct KvReadArgs {
+  KvGeometry g;
+  void* y[2] = {};              // K, V rows out (either may be null)
+  const float* Dr[2] = {};
+};
+cudaError_t launch_kv_read(const KvReadArgs& a, int hd, int bits, int group, int dtype,
+                           int num_sms, cudaStream_t stream);
+
+struct KvAttentionArgs {
+  KvGeometry g;
+  const float* Dk = nullptr;    // D^{-1/2} of K and V, or null
+  const float* Dv = nullptr;
+  const void* Q = nullptr;
+  int64_t q_row = 0, q_head = 0;
+  int q_type = kRowBF16, y_type = kRowBF16;
+  int heads = 1, per = 1;       // query heads; query heads of one key/value head
+  float scale = 1.f, cap = 0.f;
+  int64_t window = 0;
+  const uint64_t* tree = nullptr;
+  void* Y = nullptr;
+  float* part = nullptr;        // partial results, then one descriptor per block of the grid
+  int4* meta = nullptr;
+};
+// How a launch is laid out: 8 nt query rows per tile, `grid` blocks, and the
+// floats of one partial result.
+struct KvAttentionPlan {
+  int nt, grid;
+  int64_t slot_floats;
+  int64_t meta_bytes, part_bytes;
+};
+// grid 0: the format is not built.
+KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows);
+cudaError_t launch_kv_attention(const KvAttentionArgs& a, int hd, int bits, int group,
+                                const KvAttentionPlan& plan, cudaStream_t stream);
+
+}  // namespace ttq

@@ -926,8 +926,8 @@ ttq_status ttq_get_status(const void* ws, uint32_t* flags) {
 
 ttq_status ttq_status_from_flags(uint32_t flags) {
   if (flags & TTQ_FLAG_TIMEOUT) return TTQ_ERR_TIMEOUT;
-  if (flags & ~TTQ_FLAG_RANK_DEFICIENT) return TTQ_ERR_NONFINITE;
-  return TTQ_OK;
+  if (flags & ~(TTQ_FLAG_RANK_DEFICIENT | TTQ_FLAG_BAD_INDEX)) return TTQ_ERR_NONFINITE;
+  return flags & TTQ_FLAG_BAD_INDEX ? TTQ_ERR_INVALID_ARG : TTQ_OK;
 }
 
 const char* ttq_status_string(ttq_status s) {

@@ -1,5 +1,5 @@
-"""Python binding of libttq.so: the C ABI of include/ttq.h, one function per
-entry point with the same name.  Argument marshalling only -- every step of
+"""Python binding of libttq.so: the C ABI of include/ttq.h and include/ttq_kv.h,
+one function per entry point with the same name.  Argument marshalling only -- every step of
 the TTQ layer runs in the library's CUDA kernels; torch supplies device
 memory and the current stream.  There is no fallback: if the library is
 missing or the tensors are not on a CUDA device, the call raises.
@@ -35,8 +35,9 @@ TTQ_FLAG_SCALE_OVERFLOW = 0x2
 TTQ_FLAG_TIMEOUT = 0x4
 TTQ_FLAG_X_RANGE = 0x8
 TTQ_FLAG_RANK_DEFICIENT = 0x10
+TTQ_FLAG_BAD_INDEX = 0x20
 
-# C signatures, in the order of include/ttq.h
+# C signatures, in the order of include/ttq.h and include/ttq_kv.h
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
@@ -50,6 +51,20 @@ class WorkspaceLayout(ctypes.Structure):
                 ("wq", _SZ), ("total", _SZ), ("splits", _I64), ("ax_ld", _I64), ("axp", _SZ),
                 ("D_sqrt", _SZ), ("ypart", _SZ), ("tickets", _SZ), ("ax_splits", _I64)]
 
+
+class _CacheStruct(ctypes.Structure):   # ttq_kv_cache
+    _fields_ = [("pages", _P), ("num_pages", _I64), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("bits", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scheme", ctypes.c_int32), ("D_k", _P), ("D_v", _P), ("D_k_rsqrt", _P), ("D_v_rsqrt", _P)]
+
+
+class _BatchStruct(ctypes.Structure):   # ttq_kv_batch
+    _fields_ = [("page_table", _P), ("table_stride", _I64), ("kv_len", _P), ("cu_new", _P), ("batch", _I64),
+                ("rows", _I64), ("max_new", _I64)]
+
+
+_CACHE = ctypes.POINTER(_CacheStruct)
+_BATCH = ctypes.POINTER(_BatchStruct)
 
 SIGNATURES = {
     "ttq_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _INT, _INT, _INT]),
@@ -82,6 +97,12 @@ SIGNATURES = {
     "ttq_status_from_flags": (_INT, [ctypes.c_uint32]),
     "ttq_lowrank_workspace_size": (_SZ, [_I64, _I64, _I64, _I64]),
     "ttq_lowrank_init": (_INT, [_P, _INT, _I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _SZ, _P]),
+    "ttq_kv_page_bytes": (_SZ, [_INT, _INT, _INT, _INT, _INT]),
+    "ttq_kv_write": (_INT, [_CACHE, _BATCH, _P, _I64, _I64, _P, _I64, _I64, _INT, _P, _SZ, _P]),
+    "ttq_kv_read": (_INT, [_CACHE, _BATCH, _P, _P, _INT, _P, _SZ, _P]),
+    "ttq_kv_attention_workspace_size": (_SZ, [_INT, _INT, _INT, _I64, _I64, _I64]),
+    "ttq_kv_attention": (_INT, [_CACHE, _BATCH, _P, _I64, _I64, _INT, _I64, _F, _F, _I64, _P, _P, _INT, _P, _SZ,
+                                _P]),
     "ttq_status_string": (ctypes.c_char_p, [_INT]),
     "ttq_version": (ctypes.c_char_p, []),
 }
@@ -618,3 +639,216 @@ def workspace_views(ws: torch.Tensor, d, dp, T, r, bits, group, dtype=TTQ_BF16) 
         if L.wq:
             out["wq"] = view(L.wq, dp * d, torch.float16).view(dp, d)
     return out
+
+
+# --------------------------------------------- the quantised key/value cache
+_ROW_TYPES = (torch.float32, torch.bfloat16, torch.float16)
+
+
+def _ints(t: torch.Tensor, name: str, shape) -> None:
+    """t is int32 of this shape (None: any size there)."""
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.int32")
+    if t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}")
+
+
+def _rows_of(t: torch.Tensor, name: str, rows: int, heads, head_dim: int) -> None:
+    """t is [rows][heads][head_dim] with contiguous channels (heads None: any number)."""
+    if t.dtype not in _ROW_TYPES:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {list(_ROW_TYPES)}")
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, '*' if heads is None else heads, head_dim)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"the channels of {name} must be contiguous, got strides {t.stride()}")
+
+
+def _strided(t: torch.Tensor, name: str) -> tuple:
+    """(pointer, row stride, head stride) of a row tensor on the current device."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    cur = torch.cuda.current_device()
+    if t.device.index != cur:
+        raise ValueError(f"{name} is on {t.device}; the library runs on the current device cuda:{cur}")
+    # the stride of a size that is not walked along says nothing
+    row, head = t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+    if row % 8 or head % 8 or t.data_ptr() % 16:
+        raise ValueError(f"the rows of {name} must be 16-byte aligned: strides {t.stride()} are not multiples of 8 "
+                         "elements, or its first element is not at a 16-byte boundary")
+    return t.data_ptr(), row, head
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised tensor of the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class KVCache:
+    """A quantised key/value cache (ttq_kv_cache): `pages` uint8 [num_pages][ttq_kv_page_bytes(...)] (new_kv_cache
+    makes it) and its format; D_k, D_v and their inverse square roots float32 [kv_heads][head_dim] or None, as
+    ttq_act_norm gives them for rows of K and V.  It keeps the tensors; replacing one takes a new KVCache."""
+
+    def __init__(self, pages, page_size, kv_heads, head_dim, bits, group, scheme=TTQ_QSCHEME_ASYMMETRIC, D_k=None,
+                 D_v=None, D_k_rsqrt=None, D_v_rsqrt=None):
+        n = ttq_kv_page_bytes(page_size, kv_heads, head_dim, bits, group)
+        if pages.dtype != torch.uint8 or pages.dim() != 2 or pages.shape[1] != n:
+            raise ValueError(f"pages must be uint8 [num_pages][{n}], got {pages.dtype} {tuple(pages.shape)}")
+        for t, name in ((D_k, "D_k"), (D_v, "D_v"), (D_k_rsqrt, "D_k_rsqrt"), (D_v_rsqrt, "D_v_rsqrt")):
+            _vector(t, name, kv_heads * head_dim)
+        for a, b, name in ((D_k, D_k_rsqrt, "k"), (D_v, D_v_rsqrt, "v")):
+            if (a is None) != (b is None):
+                raise ValueError(f"D_{name} and D_{name}_rsqrt are given together or not at all")
+        self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, kv_heads, head_dim
+        self.bits, self.group, self.scheme = bits, group, scheme
+        self.D_k, self.D_v, self.D_k_rsqrt, self.D_v_rsqrt = D_k, D_v, D_k_rsqrt, D_v_rsqrt
+        self._struct = None
+
+    def _arg(self):
+        if self._struct is None:
+            self._struct = _CacheStruct(_dev(self.pages, "pages"), self.pages.shape[0], self.page_size, self.kv_heads,
+                                        self.head_dim, self.bits, self.group, self.scheme, _dev(self.D_k, "D_k"),
+                                        _dev(self.D_v, "D_v"), _dev(self.D_k_rsqrt, "D_k_rsqrt"),
+                                        _dev(self.D_v_rsqrt, "D_v_rsqrt"))
+            self._ref = ctypes.byref(self._struct)
+        elif self.pages.device.index != torch.cuda.current_device():
+            raise ValueError(f"pages is on {self.pages.device}; the library runs on the current device "
+                             f"cuda:{torch.cuda.current_device()}")
+        return self._ref
+
+
+class KVBatch:
+    """The rows of a call (ttq_kv_batch): sequence i has rows cu_new[i] .. cu_new[i + 1] - 1, its last positions of
+    kv_len[i]; page_table int32 [batch][pages], kv_len int32 [batch], cu_new int32 [batch + 1] (device tensors whose
+    contents may change between calls), `rows` rows in the row tensors, at most max_new of any sequence."""
+
+    def __init__(self, page_table, kv_len, cu_new, rows, max_new):
+        _ints(kv_len, "kv_len", (None,))
+        n = kv_len.shape[0]
+        _ints(cu_new, "cu_new", (n + 1,))
+        _ints(page_table, "page_table", (n, None))
+        if rows < 0 or max_new < 0:
+            raise ValueError(f"rows and max_new must not be negative, got {rows} and {max_new}")
+        self.page_table, self.kv_len, self.cu_new, self.rows, self.max_new = page_table, kv_len, cu_new, rows, max_new
+        self._struct = None
+
+    def _arg(self, cache):
+        if self._struct is None:
+            self._struct = _BatchStruct(_dev(self.page_table, "page_table"), self.page_table.shape[1],
+                                        _dev(self.kv_len, "kv_len"), _dev(self.cu_new, "cu_new"), self.kv_len.shape[0],
+                                        self.rows, self.max_new)
+            self._ref = ctypes.byref(self._struct)
+        if self.kv_len.device != cache.pages.device:
+            raise ValueError(f"the batch is on {self.kv_len.device}, the cache on {cache.pages.device}")
+        return self._ref
+
+
+def ttq_kv_page_bytes(page_size, kv_heads, head_dim, bits, group) -> int:
+    """Bytes of one page of a key/value cache (raises if the format is not built)."""
+    n = int(lib().ttq_kv_page_bytes(page_size, kv_heads, head_dim, bits, group))
+    if n == 0:
+        raise TTQError(TTQ_ERR_UNSUPPORTED, "ttq_kv_page_bytes")
+    return n
+
+
+def new_kv_cache(num_pages, page_size, kv_heads, head_dim, bits, group, scheme=TTQ_QSCHEME_ASYMMETRIC, device="cuda",
+                 **statistics) -> KVCache:
+    """A KVCache of num_pages uninitialised pages."""
+    n = ttq_kv_page_bytes(page_size, kv_heads, head_dim, bits, group)
+    return KVCache(torch.empty((num_pages, n), dtype=torch.uint8, device=device), page_size, kv_heads, head_dim, bits,
+                   group, scheme, **statistics)
+
+
+def ttq_kv_attention_workspace_size(head_dim, bits, group, heads, kv_heads, max_new) -> int:
+    """Workspace bytes of ttq_kv_attention (0: not built)."""
+    return int(lib().ttq_kv_attention_workspace_size(head_dim, bits, group, heads, kv_heads, max_new))
+
+
+def new_kv_workspace(cache, batch, heads=None, stream=None) -> torch.Tensor:
+    """An initialised workspace for the cache's entry points: for ttq_kv_attention with `heads` query heads (None:
+    only ttq_kv_write and ttq_kv_read) and batches of at most batch.max_new rows a sequence."""
+    n = 4096
+    if heads is not None and batch.max_new <= 64:
+        n = max(n, ttq_kv_attention_workspace_size(cache.head_dim, cache.bits, cache.group, heads, cache.kv_heads,
+                                                   batch.max_new))
+    ws = _empty(n, torch.uint8, cache.pages.device, stream)
+    ttq_workspace_init(ws, stream)
+    return ws
+
+
+def ttq_kv_write(cache, batch, K, V, ws=None, stream=None) -> None:
+    """Quantises the rows of K and V [rows][kv_heads][head_dim] into the cache (one type; rows and heads may be
+    strided, as slices of a fused projection are)."""
+    _rows_of(K, "K", batch.rows, cache.kv_heads, cache.head_dim)
+    _rows_of(V, "V", batch.rows, cache.kv_heads, cache.head_dim)
+    if K.dtype != V.dtype:
+        raise TypeError(f"K and V have different dtypes {K.dtype} and {V.dtype}")
+    rows = (*_strided(K, "K"), *_strided(V, "V"))
+    c = cache._arg()
+    b = batch._arg(cache)
+    if ws is None:
+        ws = new_kv_workspace(cache, batch, None, stream)
+    _check(lib().ttq_kv_write(c, b, *rows, _dtype_code(K), _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+           "ttq_kv_write")
+
+
+def ttq_kv_read(cache, batch, K=None, V=None, dtype=None, ws=None, stream=None):
+    """The dequantised rows (K, V), each [rows][kv_heads][head_dim] in `dtype` (default bf16, or that of a given
+    tensor).  Rows in no sequence are left as they are (uninitialised in a new tensor)."""
+    for t, name in ((K, "K"), (V, "V")):
+        if t is not None:
+            _rows_of(t, name, batch.rows, cache.kv_heads, cache.head_dim)
+            if dtype is not None and t.dtype != dtype:
+                raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+            dtype = t.dtype
+    dtype = dtype or torch.bfloat16
+    if dtype not in _ROW_TYPES:
+        raise TypeError(f"unsupported dtype {dtype} (float32, bfloat16 or float16)")
+    c = cache._arg()
+    b = batch._arg(cache)
+    shape = (batch.rows, cache.kv_heads, cache.head_dim)
+    if K is None:
+        K = _empty(shape, dtype, cache.pages.device, stream)
+    if V is None:
+        V = _empty(shape, dtype, cache.pages.device, stream)
+    if ws is None:
+        ws = new_kv_workspace(cache, batch, None, stream)
+    _check(lib().ttq_kv_read(c, b, _dev(K, "K"), _dev(V, "V"), _dtype_code(K), _dev(ws, "ws"), _nbytes(ws),
+                             _stream(stream)), "ttq_kv_read")
+    return K, V
+
+
+def ttq_kv_attention(cache, batch, Q, scale, softcap=0.0, window=0, tree=None, ws=None, Y=None, y_dtype=None,
+                     stream=None):
+    """Y [rows][heads][head_dim]: attention of the batch's rows of Q (strided like K of ttq_kv_write) over the cache,
+    causal among a sequence's own rows, or by `tree` (int64 [rows]: bit k of a row's mask is set iff it sees the
+    sequence's k-th new row).  softcap: scores are softcap tanh(t / softcap); window: positions seen, 0 for all."""
+    _rows_of(Q, "Q", batch.rows, None, cache.head_dim)
+    heads = Q.shape[1]
+    if heads % cache.kv_heads or heads == 0:
+        raise ValueError(f"{heads} query heads are not a multiple of the cache's {cache.kv_heads} heads")
+    if tree is not None:
+        if tree.dtype != torch.int64:
+            raise TypeError(f"tree has dtype {tree.dtype}, expected torch.int64")
+        if tree.dim() != 1 or tree.shape[0] != batch.rows:
+            raise ValueError(f"tree has shape {tuple(tree.shape)}, expected ({batch.rows},)")
+    if Y is not None:
+        _rows_of(Y, "Y", batch.rows, heads, cache.head_dim)
+        if y_dtype is not None and Y.dtype != y_dtype:
+            raise TypeError(f"Y has dtype {Y.dtype}, expected {y_dtype}")
+    y_dtype = Y.dtype if Y is not None else (y_dtype or Q.dtype)
+    if y_dtype not in _ROW_TYPES:
+        raise TypeError(f"unsupported dtype {y_dtype} (float32, bfloat16 or float16)")
+    q = _strided(Q, "Q")
+    c = cache._arg()
+    b = batch._arg(cache)
+    if Y is None:
+        Y = _empty(Q.shape, y_dtype, Q.device, stream)
+    if ws is None:
+        ws = new_kv_workspace(cache, batch, heads, stream)
+    _check(lib().ttq_kv_attention(c, b, *q, _dtype_code(Q), heads, scale, softcap, window, _dev(tree, "tree"),
+                                  _dev(Y, "Y"), _dtype_code(Y), _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
+           "ttq_kv_attention")
+    return Y
