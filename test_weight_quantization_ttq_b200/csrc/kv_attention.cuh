@@ -49,26 +49,30 @@ constexpr float kKvSlack = 8.f;
 template <int HD, int BITS, int NG, int NT>
 struct KvAttention {
   using F = KvFormat<HD, BITS, NG>;
-  static constexpr int W = 8;                       // warps of a block
+  static constexpr int W = 4;                       // warps of a block
   static constexpr int ROWS = 8 * NT;               // query rows of a tile
   static constexpr int KS = HD / 16;                // k steps of the first product
   static constexpr int MT = HD / 16;                // m tiles of the second
   // blocks per SM by registers (HD NT / 4 accumulators a thread) and memory
   static constexpr int SM_BYTES = 208 * 1024;
-  static constexpr int FIT = SM_BYTES / 2 - 8192 - NT * KS * 256 >= W * 2 * F::BLOCK ? 2 : 1;
-  static constexpr int CTAS = HD * NT / 4 <= 64 ? FIT : 1;
-  static constexpr int ROOM = SM_BYTES / CTAS - 8192 - NT * KS * 256;
-  static constexpr int STAGES_FIT = ROOM / (W * F::BLOCK);
+  static constexpr int LDO = HD + 4;                // padded row of the merge buffer
+  static constexpr int MERGE = W * ROWS * LDO * 4;
+  static constexpr int QFRAG = NT * KS * 32 * 8;
+  static constexpr int OTHER = QFRAG + 4096;        // static arrays, and 16 bytes a sequence
+  static constexpr int room(int ctas) { return SM_BYTES / ctas - OTHER; }
+  static constexpr int fits(int ctas) { return room(ctas) >= W * 2 * F::BLOCK && room(ctas) >= MERGE; }
+  static constexpr int CTAS = HD * NT / 4 <= 64 ? (fits(4) ? 4 : fits(3) ? 3 : 2) : 2;
+  static constexpr int STAGES_FIT = room(CTAS) / (W * F::BLOCK);
   static constexpr int STAGES = STAGES_FIT > 4 ? 4 : STAGES_FIT;
   static_assert(STAGES >= 2, "the ring needs two stages");
-  static constexpr int LDO = HD + 4;                // padded row of the merge buffer
   static constexpr int RING = W * STAGES * F::BLOCK;
-  static constexpr int MERGE = W * ROWS * LDO * 4;
   static constexpr int UNION = RING > MERGE ? RING : MERGE;
-  static constexpr int QFRAG = NT * KS * 32 * 8;
   // dynamic shared memory: ring / merge | Q fragments | sequences (16 B each)
   static constexpr int SMEM = UNION + QFRAG;
   static constexpr int SLOT = ROWS * (HD + 2);      // floats of a partial result
+  // what a segment costs besides its blocks, in blocks: its rows of Q, the
+  // first copy's latency and the merge
+  static constexpr int OVERHEAD = 8;
 };
 
 __device__ __forceinline__ void kv_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -166,11 +170,39 @@ struct KvSegment {
   int blocks;            // and how many there are
 };
 
-// float32 element `at` of a row tensor of the given type.
-__device__ __forceinline__ float kv_element(const void* p, int type, int64_t at) {
-  if (type == kRowF32) return static_cast<const float*>(p)[at];
-  if (type == kRowBF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
-  return __half2float(static_cast<const __half*>(p)[at]);
+// E (2, 4 or 8) consecutive elements of a row tensor of the given type.
+template <int E>
+__device__ __forceinline__ void kv_load_lane(const void* p, int type, int64_t at, float (&v)[E]) {
+  if (type == kRowF32) {
+    const float2* s = reinterpret_cast<const float2*>(static_cast<const float*>(p) + at);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const float2 f = s[e];
+      v[2 * e] = f.x, v[2 * e + 1] = f.y;
+    }
+    return;
+  }
+  uint32_t w[E / 2];
+  const uint16_t* s = static_cast<const uint16_t*>(p) + at;
+  if constexpr (E == 2) w[0] = *reinterpret_cast<const uint32_t*>(s);
+  if constexpr (E == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(s);
+    w[0] = u.x, w[1] = u.y;
+  }
+  if constexpr (E == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(s);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  }
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) {
+    if (type == kRowBF16) {
+      v[2 * e] = __uint_as_float(w[e] << 16);
+      v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(u32_as_h2(w[e]));
+      v[2 * e] = f.x, v[2 * e + 1] = f.y;
+    }
+  }
 }
 // Four consecutive elements, rounded to the type.
 __device__ __forceinline__ void kv_store4(void* p, int type, int64_t at, float4 v) {
@@ -252,7 +284,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     KvSequence s;
     int64_t w = 0;
     if (kv_sequence(g, b, s)) {
-      if (s.n > 0) w = static_cast<int64_t>(((s.kv - 1) >> 4) + 1 - first_block(s.kv, s.n)) * tiles_of(s.n);
+      if (s.n > 0) w = static_cast<int64_t>(((s.kv - 1) >> 4) + 1 - first_block(s.kv, s.n) + A::OVERHEAD) * tiles_of(s.n);
     } else {
       if (blockIdx.x == 0 && s.n != 0) set_flag(g.status, TTQ_FLAG_BAD_INDEX);
       s.n = 0;
@@ -277,9 +309,10 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
   }
   __syncthreads();
   const int64_t total = g.batch > 0 ? end_of(seqs[g.batch - 1]) * g.kv_heads : 0;
-  // no fewer than 2 blocks of tokens per warp, so that short contexts are not
-  // cut into pieces whose merge costs more than they do
-  const int64_t most = (total + 2 * W - 1) / (2 * W);
+  // no run shorter than a segment's overhead and 2 blocks a warp, so that short
+  // contexts are not cut into pieces whose merge costs more than they do
+  constexpr int LEAST = A::OVERHEAD + 2 * W;
+  const int64_t most = (total + LEAST - 1) / LEAST;
   const int64_t runs = most < static_cast<int64_t>(gridDim.x) ? most : static_cast<int64_t>(gridDim.x);
   int4* meta = a.meta + 2 * blockIdx.x;
   if (tid == 0) meta[0] = make_int4(-1, 0, 0, 0);
@@ -287,30 +320,51 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
   int64_t x = blockIdx.x * total / runs;
   const int64_t x1 = (blockIdx.x + 1) * total / runs;
 
+  // ---- the segment at x; a segment's blocks follow A::OVERHEAD units of its
+  // own cost, so a run that begins within those begins with its first block
+  KvSegment seg;
+  int from, tiles;
+  int64_t left = 0;                             // units of the segment from x on
+  auto enter = [&](int b) {                     // sequence b's first segment
+    while (((seqs[b].y >> 24) & 0xFF) == 0) ++b;   // there is one: x < total
+    const int4 q = seqs[b];
+    seg.b = b, seg.h = 0, seg.tile = 0, seg.kv = q.z, seg.row0 = q.w, seg.n = q.y >> 24;
+    seg.first = first_block(seg.kv, seg.n);
+    seg.blocks = ((seg.kv - 1) >> 4) + 1 - seg.first;
+    tiles = tiles_of(seg.n);
+  };
+  {
+    const int64_t per_head_x = x / g.kv_heads;
+    int lo = 0, hi = g.batch - 1;               // first b with end * kv_heads > x
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (end_of(seqs[mid]) > per_head_x) hi = mid; else lo = mid + 1;
+    }
+    enter(lo);
+    const int64_t rest = x - (lo > 0 ? end_of(seqs[lo - 1]) * g.kv_heads : 0);
+    const int64_t units = seg.blocks + A::OVERHEAD, tile = rest / units;
+    left = units - (rest - tile * units);
+    seg.h = static_cast<int>(tile / tiles);
+    seg.tile = static_cast<int>(tile - static_cast<int64_t>(seg.h) * tiles);
+  }
   uint32_t phases = 0;                          // bit s: parity of stage s
   for (bool started = false; x < x1; started = true) {
-    // ---- the segment at x
-    KvSegment seg;
-    int from, count;
-    {
-      const int64_t per_head_x = x / g.kv_heads;      // a bound for the search below
-      int lo = 0, hi = g.batch - 1;                   // first b with end * kv_heads > x
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (end_of(seqs[mid]) > per_head_x) hi = mid; else lo = mid + 1;
+    if (started && left == 0) {                 // the next segment
+      if (++seg.tile == tiles) {
+        seg.tile = 0;
+        if (++seg.h == g.kv_heads) enter(seg.b + 1);
       }
-      const int4 q = seqs[lo];
-      const int64_t begin = lo > 0 ? end_of(seqs[lo - 1]) * g.kv_heads : 0;
-      seg.b = lo, seg.kv = q.z, seg.row0 = q.w, seg.n = q.y >> 24;
-      seg.first = first_block(seg.kv, seg.n);
-      seg.blocks = ((seg.kv - 1) >> 4) + 1 - seg.first;
-      const int64_t rest = x - begin, tile = rest / seg.blocks;
-      from = static_cast<int>(rest - tile * seg.blocks);
-      const int tiles = tiles_of(seg.n);
-      seg.h = static_cast<int>(tile / tiles);
-      seg.tile = static_cast<int>(tile - static_cast<int64_t>(seg.h) * tiles);
-      count = static_cast<int>(x1 - x < seg.blocks - from ? x1 - x : seg.blocks - from);
+      left = seg.blocks + A::OVERHEAD;
     }
+    // blocks [from, from + count) of it are this run's; none if only a part
+    // of its overhead is
+    const int64_t take = x1 - x < left ? x1 - x : left;
+    const int end = seg.blocks - static_cast<int>(left - take < seg.blocks ? left - take : seg.blocks);
+    from = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks);
+    const int count = end - from;
+    x += take;
+    left -= take;
+    if (count == 0) continue;
     const bool whole = from == 0 && count == seg.blocks;
     const int old = seg.kv - seg.n;             // positions before the new ones
     const int R = seg.n * a.per, r0 = seg.tile * ROWS;
@@ -351,45 +405,59 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     for (; issued < STAGES && issued < mine; ++issued) issue(issued);
 
     // ---- the tile's rows of Q as B fragments, and what each row sees
-    for (int r = warp; r < ROWS; r += W) {
-      const int rr = r0 + r;
+    {
       constexpr int E = HD / 32;                // consecutive channels of a lane
-      const int ch = lane * E, i_new = rr / a.per;
-      float v[E];
-      float big = 0.f;
+      constexpr int RW = ROWS / W;              // rows of a warp
+      float v[RW][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        v[e] = 0.f;
+      for (int k = 0; k < RW; ++k) {
+        const int rr = r0 + warp * RW + k;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] = 0.f;
         if (rr < R) {
-          v[e] = kv_element(a.Q, a.q_type, (seg.row0 + i_new) * a.q_row + (seg.h * a.per + rr % a.per) * a.q_head + ch + e);
-          if (a.Dk != nullptr) v[e] *= __ldg(a.Dk + seg.h * HD + ch + e);
+          const int i_new = rr / a.per;
+          kv_load_lane<E>(a.Q, a.q_type,
+                          (seg.row0 + i_new) * a.q_row + (seg.h * a.per + rr - i_new * a.per) * a.q_head + lane * E, v[k]);
         }
-        big = fmaxf(big, fabsf(v[e]));
       }
+      float dk[E];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      int ex = static_cast<int>(__float_as_uint(big) >> 23);
-      ex = min(max(ex, 1), 253);
-      const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^-(ex - 127)
-      const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+      for (int e = 0; e < E; ++e) dk[e] = a.Dk != nullptr ? __ldg(a.Dk + seg.h * HD + lane * E + e) : 1.f;
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const int c = ch + e, k = c / F::G, j = c % F::G;
-        const int quarter = j / (F::G / 4), idx = k * (F::G / 4) + j % (F::G / 4);
-        qfrag[(((r >> 3) * KS + idx / 4) * 32 + 4 * (r & 7) + quarter) * 2 + (idx % 4) / 2] =
-            h2_as_u32(__floats2half2_rn(v[e] * down, v[e + 1] * down));
+      for (int k = 0; k < RW; ++k) {
+        const int r = warp * RW + k;
+        float big = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          v[k][e] *= dk[e];
+          big = fmaxf(big, fabsf(v[k][e]));
+        }
+        // the row's largest magnitude: bits of non-negative floats order as integers
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+        const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
+        const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^-(ex - 127)
+        const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const int c = lane * E + e, kg = c / F::G, j = c % F::G;
+          const int quarter = j / (F::G / 4), idx = kg * (F::G / 4) + j % (F::G / 4);
+          qfrag[(((r >> 3) * KS + idx / 4) * 32 + 4 * (r & 7) + quarter) * 2 + (idx % 4) / 2] =
+              h2_as_u32(__floats2half2_rn(v[k][e] * down, v[k][e + 1] * down));
+        }
+        if (lane == 0) q_factor[r] = a.scale * up * (a.cap > 0.f ? 1.f / a.cap : kKvLog2e);
       }
-      if (lane == 0) {
-        q_factor[r] = a.scale * up * (a.cap > 0.f ? 1.f / a.cap : kKvLog2e);
+      if (tid < ROWS) {
+        const int rr = r0 + tid, i_new = rr / a.per;
         uint64_t mask = 0;
         if (rr < R) mask = a.tree != nullptr ? a.tree[seg.row0 + i_new] : (2ull << i_new) - 1ull;
-        row_mask[r] = mask;
-        row_pos[r] = old + __popcll(mask & ~(1ull << (i_new & 63)));
+        row_mask[tid] = mask;
+        row_pos[tid] = old + __popcll(mask & ~(1ull << (i_new & 63)));
       }
-    }
-    for (int i = tid; i < seg.n; i += W * 32) {
-      const uint64_t mask = a.tree != nullptr ? a.tree[seg.row0 + i] : (2ull << i) - 1ull;
-      new_pos[i] = old + __popcll(mask & ~(1ull << i));
+      if (tid >= 64 && tid - 64 < seg.n) {
+        const int i = tid - 64;
+        const uint64_t mask = a.tree != nullptr ? a.tree[seg.row0 + i] : (2ull << i) - 1ull;
+        new_pos[i] = old + __popcll(mask & ~(1ull << i));
+      }
     }
     __syncthreads();
 
@@ -707,12 +775,11 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       }
     }
     if (tid == 0 && from == 0 && !whole) {
-      // the run that holds the segment's last block: the last i with i total / runs <= x
-      const int64_t last = x + seg.blocks - 1;
+      // the run that holds the segment's last block: the last i with i total / runs <= its place
+      const int64_t last = x + left - 1;
       meta[0] = make_int4(static_cast<int>(((last + 1) * runs - 1) / total), seg.row0, seg.h, r0);
       meta[1] = make_int4(R, 0, 0, 0);
     }
-    x += count;
     if (failed) return;      // the same for all threads: set before the barriers above
   }
 }
