@@ -499,8 +499,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               if constexpr (BITS == 8) {
-                pa[r][0] = kv_e4m3x2(kw[r][w]);
-                pa[r][1] = kv_e4m3x2(kw[r][w] >> 16);
+                kv_e4m3x4(kw[r][w], pa[r][0], pa[r][1]);
               } else {
                 kv_int_pairs<BITS>(kw[r][w], z[r], pa[r]);
               }
@@ -658,9 +657,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               if constexpr (BITS == 8) {        // bytes: even token's two channels, then the odd one's
-                const uint32_t v = __byte_perm(vw[r][w], 0, 0x3120);
-                pv[r][0] = kv_e4m3x2(v);
-                pv[r][1] = kv_e4m3x2(v >> 16);
+                kv_e4m3x4(__byte_perm(vw[r][w], 0, 0x3120), pv[r][0], pv[r][1]);
               } else {
                 kv_int_pairs<BITS>(vw[r][w], z[r], pv[r]);
               }
@@ -785,34 +782,57 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 }
 
 // Merges the partial results of the segment that began in run blockIdx.x and
-// went on into later runs, in their order.
+// went on into later runs: a block takes one row, its threads are the float4
+// channels of the row times slices of the partial results, which are
+// summed per slice and then over the slices, always in the same order.
+constexpr int kKvJoinThreads = 256;
 template <int HD, int ROWS>
-__global__ void __launch_bounds__(256) kv_join_kernel(const KvAttentionArgs a) {
-  constexpr int SLOT = ROWS * (HD + 2);
+__global__ void __launch_bounds__(kKvJoinThreads) kv_join_kernel(const KvAttentionArgs a) {
+  constexpr int SLOT = ROWS * (HD + 2), LANES = HD / 4, SLICES = kKvJoinThreads / LANES;
+  __shared__ float4 acc_s[SLICES][LANES];
+  __shared__ float sum_s[SLICES];
   allow_dependents_launch();
   grid_dependency_wait();
   const int4 m0 = a.meta[2 * blockIdx.x];
   if (m0.x < 0) return;
   const int R = a.meta[2 * blockIdx.x + 1].x;
-  const int first = blockIdx.x, last = m0.x, row0 = m0.y, h = m0.z, r0 = m0.w;
-  const int i = blockIdx.y * 256 + threadIdx.x;
-  if (i >= ROWS * (HD / 4)) return;
-  const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
+  const int first = blockIdx.x, last = m0.x, row0 = m0.y, h = m0.z, r0 = m0.w, r = blockIdx.y;
   if (r0 + r >= R) return;
-  float mx = kKvFloor, sum = 0.f;
+  const int slice = threadIdx.x / LANES, ch = (threadIdx.x % LANES) * 4;
+  // partial result k of the segment is in the first slot of run first + k, but for k = 0
+  auto slot_of = [&](int k) { return a.part + (2 * static_cast<int64_t>(first + k) + (k == 0 ? 1 : 0)) * SLOT; };
+  const int n = last - first + 1;
+  float mx = kKvFloor;
+  for (int k = threadIdx.x; k < n; k += kKvJoinThreads) mx = fmaxf(mx, slot_of(k)[ROWS * HD + r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  __shared__ float max_s[kKvJoinThreads / 32];
+  if (threadIdx.x % 32 == 0) max_s[threadIdx.x / 32] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kKvJoinThreads / 32; ++w) mx = fmaxf(mx, max_s[w]);
+  float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = first; k <= last; ++k) {
-    const float* slot = a.part + (2 * static_cast<int64_t>(k) + (k == first ? 1 : 0)) * SLOT;
+#pragma unroll 4
+  for (int k = slice; k < n; k += SLICES) {
+    const float* slot = slot_of(k);
     const float4 v = *reinterpret_cast<const float4*>(slot + r * HD + ch);
-    const float mk = slot[ROWS * HD + r], lk = slot[ROWS * HD + ROWS + r];
-    const float m_new = fmaxf(mx, mk);
-    const float f = kv_exp2(mx - m_new), fk = kv_exp2(mk - m_new);
-    mx = m_new;
-    sum = fmaf(lk, fk, sum * f);
-    acc.x = fmaf(v.x, fk, acc.x * f);
-    acc.y = fmaf(v.y, fk, acc.y * f);
-    acc.z = fmaf(v.z, fk, acc.z * f);
-    acc.w = fmaf(v.w, fk, acc.w * f);
+    const float f = kv_exp2(slot[ROWS * HD + r] - mx);
+    sum = fmaf(slot[ROWS * HD + ROWS + r], f, sum);
+    acc.x = fmaf(v.x, f, acc.x);
+    acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z);
+    acc.w = fmaf(v.w, f, acc.w);
+  }
+  acc_s[slice][threadIdx.x % LANES] = acc;
+  if (ch == 0) sum_s[slice] = sum;
+  __syncthreads();
+  if (slice != 0) return;
+#pragma unroll
+  for (int w = 1; w < SLICES; ++w) {
+    const float4 v = acc_s[w][threadIdx.x];
+    sum += sum_s[w];
+    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
   }
   kv_store_row<HD>(a, row0, h, r0 + r, ch, acc, sum);
 }
@@ -879,8 +899,7 @@ cudaError_t kv_attention_launch(const KvAttentionArgs& a, int bits, int group, c
     }
     e = launch_kernel(kernel, dim3(p.grid), dim3(A::W * 32), smem, stream, true, a);
     if (e != cudaSuccess) return;
-    const dim3 grid(p.grid, (A::ROWS * (HD / 4) + 255) / 256);
-    e = launch_kernel(kv_join_kernel<HD, A::ROWS>, grid, dim3(256), 0, stream, true, a);
+    e = launch_kernel(kv_join_kernel<HD, A::ROWS>, dim3(p.grid, A::ROWS), dim3(kKvJoinThreads), 0, stream, true, a);
   });
   return e;
 }

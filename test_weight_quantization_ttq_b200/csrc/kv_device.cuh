@@ -85,10 +85,16 @@ __device__ __forceinline__ __half2 u32_as_h2(uint32_t u) {
   return v;
 }
 
-// Two E4M3 codes (low 16 bits) as a binary16 pair: exact.
+// Two E4M3 codes (low 16 bits) as a binary16 pair, and the two pairs of a
+// word: exact.
 __device__ __forceinline__ uint32_t kv_e4m3x2(uint32_t v) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+  uint32_t h;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(v));
+  return h;
+}
+__device__ __forceinline__ void kv_e4m3x4(uint32_t v, uint32_t& p0, uint32_t& p1) {
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}" : "=r"(p0), "=r"(p1) : "r"(v));
 }
 
 // NaN-keeping minimum and maximum.
