@@ -96,8 +96,10 @@ KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows
                                : kv_attention_ctas_hd256(bits, group, p.nt);
   p.grid = ctas * kKvPlanSMs;
   p.slot_floats = static_cast<int64_t>(8 * p.nt) * (hd + 2);
-  p.meta_bytes = static_cast<int64_t>(p.grid) * 2 * sizeof(int4);
-  p.part_bytes = 2 * p.grid * p.slot_floats * 4;
+  const int64_t warps = static_cast<int64_t>(p.grid) * kKvAttentionWarps;
+  p.meta_bytes = warps * 2 * sizeof(int4);
+  p.together_bytes = (p.grid * 4 + 255) / 256 * 256;
+  p.part_bytes = warps * 2 * p.slot_floats * 4;
   return p;
 }
 
@@ -156,7 +158,7 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
   if (max_new < 0 || max_new > kKvMaxNew) return 0;
   const KvAttentionPlan p = kv_attention_plan(head_dim, bits, group, max_new * (heads / kv_heads));
   if (p.grid == 0) return 0;
-  return kKvHeader + p.meta_bytes + p.part_bytes;
+  return kKvHeader + p.meta_bytes + p.together_bytes + p.part_bytes;
 }
 
 ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch, const void* Q,
@@ -193,7 +195,8 @@ ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch
   a.tree = tree;
   a.Y = Y;
   a.meta = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kKvHeader);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kKvHeader + p.meta_bytes);
+  a.together = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kKvHeader + p.meta_bytes);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kKvHeader + p.meta_bytes + p.together_bytes);
   return status_of(launch_kv_attention(a, cache->head_dim, cache->bits, cache->group, p,
                                        static_cast<cudaStream_t>(stream)));
 }

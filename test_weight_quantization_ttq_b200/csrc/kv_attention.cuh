@@ -7,15 +7,16 @@
 // Work.  The rows of one key/value head (its query heads x the sequence's
 // new tokens) form tiles of 8 NT rows; a segment is one (sequence, head,
 // tile) with all blocks of 16 tokens that it may see.  All segments'
-// blocks, laid end to end, are cut into equal runs, one per thread block of
-// the grid, so that contexts of any lengths load the SMs evenly; a segment
-// cut by a run's end leaves partial results (running maximum, sum and
-// accumulator) in the workspace, which kv_join_kernel merges in order.
+// blocks, laid end to end, are cut into equal runs, one per warp of the
+// grid, so that contexts of any lengths load the SMs evenly and no warp
+// waits for another; a segment cut by a run's end leaves partial results
+// (running maximum, sum and accumulator) in the workspace, which
+// kv_join_kernel merges in a fixed order.  Where all warps of a thread block
+// work on one segment, they merge theirs first.
 //
-// A warp takes every W-th block of its segment through a ring of shared
-// memory stages, one bulk copy per block (codes and pairs of K and V
-// together), and keeps its own softmax state; the warps' states are merged
-// once per segment.  Products are m16n8k16 with the codes as the A operand:
+// A warp brings its blocks through a ring of shared memory stages by bulk
+// copies (codes and pairs of K and V of a block are contiguous), BP blocks a
+// stage.  Products are m16n8k16 with the codes as the A operand:
 //   S^T [16 tokens x 8 rows] = (c - z)_K Q^T   per group of channels, then
 //       scaled by the token's s_K in fp32;
 //   O^T [channels x 8 rows] += (c - z)_V^T (p s_V)^T.
@@ -49,30 +50,38 @@ constexpr float kKvSlack = 8.f;
 template <int HD, int BITS, int NG, int NT>
 struct KvAttention {
   using F = KvFormat<HD, BITS, NG>;
-  static constexpr int W = 4;                       // warps of a block
+  static constexpr int W = kKvAttentionWarps;       // warps of a block
   static constexpr int ROWS = 8 * NT;               // query rows of a tile
   static constexpr int KS = HD / 16;                // k steps of the first product
   static constexpr int MT = HD / 16;                // m tiles of the second
-  // blocks per SM by registers (HD NT / 4 accumulators a thread) and memory
-  static constexpr int SM_BYTES = 208 * 1024;
-  static constexpr int LDO = HD + 4;                // padded row of the merge buffer
-  static constexpr int MERGE = W * ROWS * LDO * 4;
-  static constexpr int QFRAG = NT * KS * 32 * 8;
-  static constexpr int OTHER = QFRAG + 4096;        // static arrays, and 16 bytes a sequence
-  static constexpr int room(int ctas) { return SM_BYTES / ctas - OTHER; }
-  static constexpr int fits(int ctas) { return room(ctas) >= W * 2 * F::BLOCK && room(ctas) >= MERGE; }
-  static constexpr int CTAS = HD * NT / 4 <= 64 ? (fits(4) ? 4 : fits(3) ? 3 : 2) : 2;
-  static constexpr int STAGES_FIT = room(CTAS) / (W * F::BLOCK);
+  static constexpr int QFRAG = NT * KS * 32 * 8;    // a warp's Q fragments
+  static constexpr int ROWINFO = ROWS * 16;         // and what it knows of its rows
+  // Blocks of threads per SM: by registers 4 where a thread's HD NT / 4
+  // accumulators are at most 32 (128 registers), 3 for 64 (168), else 2; fewer
+  // where their rings would not have two stages.  A stage holds 2 blocks of
+  // tokens, so that its wait, vote and masks are paid once, where the scores
+  // of 32 tokens fit those registers (NT = 1) and two such stages the memory.
+  static constexpr int SM_BYTES = 212 * 1024;
+  static constexpr int room(int ctas) { return SM_BYTES / (ctas * W) - QFRAG - ROWINFO - 512; }
+  static constexpr int BY_REGS = HD * NT / 4 <= 32 ? 4 : HD * NT / 4 <= 64 ? 3 : 2;
+  static constexpr int CTAS = BY_REGS >= 4 && room(4) >= 2 * F::BLOCK ? 4 : BY_REGS >= 3 && room(3) >= 2 * F::BLOCK ? 3 : 2;
+  static constexpr int BP = NT == 1 && room(CTAS) >= 4 * F::BLOCK ? 2 : 1;
+  static constexpr int warp_room = room(CTAS);
+  static constexpr int STAGES_FIT = warp_room / (BP * F::BLOCK);
   static constexpr int STAGES = STAGES_FIT > 4 ? 4 : STAGES_FIT;
   static_assert(STAGES >= 2, "the ring needs two stages");
-  static constexpr int RING = W * STAGES * F::BLOCK;
-  static constexpr int UNION = RING > MERGE ? RING : MERGE;
-  // dynamic shared memory: ring / merge | Q fragments | sequences (16 B each)
-  static constexpr int SMEM = UNION + QFRAG;
+  static constexpr int STAGE = BP * F::BLOCK;
+  static constexpr int WARP_BYTES = STAGES * STAGE + QFRAG + ROWINFO;
+  static constexpr int LDO = HD + 4;                // padded row of the merge buffer
+  static constexpr int MERGE = W * ROWS * LDO * 4;
+  static constexpr int MAIN = W * WARP_BYTES > MERGE ? W * WARP_BYTES : MERGE;
+  // dynamic shared memory: the warps' regions (in the end the merge buffer),
+  // then 16 bytes a sequence
+  static constexpr int SMEM = MAIN;
   static constexpr int SLOT = ROWS * (HD + 2);      // floats of a partial result
   // what a segment costs besides its blocks, in blocks: its rows of Q, the
-  // first copy's latency and the merge
-  static constexpr int OVERHEAD = 8;
+  // first copy's latency and its end
+  static constexpr int OVERHEAD = 2;
 };
 
 __device__ __forceinline__ void kv_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -141,24 +150,46 @@ struct KvZero {
   }
 };
 
+// (w & MASK) | magic in one instruction: a LOP3 takes one constant, so the
+// other has to be in a register (left to the compiler it became two; with
+// half of all instructions of the loop here, 149 of 474 per block were these).
+template <uint32_t MASK>
+__device__ __forceinline__ __half2 kv_field(uint32_t w, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(magic));
+  return u32_as_h2(r);
+}
+
+// The offsets under which the fields of a word's halves count as integers.
+template <int BITS>
+struct KvMagic {
+  uint32_t v[4];
+  __device__ __forceinline__ KvMagic() {
+    // kept opaque, so that they stay in registers
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(v[0]));
+    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(v[1]));
+    if constexpr (BITS == 2) {
+      asm volatile("mov.b32 %0, 0x5C005C00;" : "=r"(v[2]));
+      asm volatile("mov.b32 %0, 0x4C004C00;" : "=r"(v[3]));
+    }
+  }
+};
+
 // The pairs (c - z) of a word of INT codes: p[i] holds the i-th field of the
 // low and of the high half.
 template <int BITS>
-__device__ __forceinline__ void kv_int_pairs(uint32_t w, const KvZero<BITS>& z, uint32_t* p) {
-  if constexpr (BITS == 4) {
-    const uint32_t u = w >> 8;
-    p[0] = h2_as_u32(__hsub2(u32_as_h2((w & 0x000F000Fu) | 0x64006400u), z.o[0]));
-    p[1] = h2_as_u32(__hsub2(u32_as_h2((w & 0x00F000F0u) | 0x54005400u), z.o[1]));
-    p[2] = h2_as_u32(__hsub2(u32_as_h2((u & 0x000F000Fu) | 0x64006400u), z.o[0]));
-    p[3] = h2_as_u32(__hsub2(u32_as_h2((u & 0x00F000F0u) | 0x54005400u), z.o[1]));
-  } else {
+__device__ __forceinline__ void kv_int_pairs(uint32_t w, const KvZero<BITS>& z, const KvMagic<BITS>& c, uint32_t* p) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t u = i ? w >> 8 : w;
-      p[4 * i] = h2_as_u32(__hsub2(u32_as_h2((u & 0x00030003u) | 0x64006400u), z.o[0]));
-      p[4 * i + 1] = h2_as_u32(__hsub2(u32_as_h2((u & 0x000C000Cu) | 0x5C005C00u), z.o[1]));
-      p[4 * i + 2] = h2_as_u32(__hsub2(u32_as_h2((u & 0x00300030u) | 0x54005400u), z.o[2]));
-      p[4 * i + 3] = h2_as_u32(__hsub2(u32_as_h2((u & 0x00C000C0u) | 0x4C004C00u), z.o[3]));
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = i ? w >> 8 : w;
+    if constexpr (BITS == 4) {
+      p[2 * i] = h2_as_u32(__hsub2(kv_field<0x000F000Fu>(u, c.v[0]), z.o[0]));
+      p[2 * i + 1] = h2_as_u32(__hsub2(kv_field<0x00F000F0u>(u, c.v[1]), z.o[1]));
+    } else {
+      p[4 * i] = h2_as_u32(__hsub2(kv_field<0x00030003u>(u, c.v[0]), z.o[0]));
+      p[4 * i + 1] = h2_as_u32(__hsub2(kv_field<0x000C000Cu>(u, c.v[2]), z.o[1]));
+      p[4 * i + 2] = h2_as_u32(__hsub2(kv_field<0x00300030u>(u, c.v[1]), z.o[2]));
+      p[4 * i + 3] = h2_as_u32(__hsub2(kv_field<0x00C000C0u>(u, c.v[3]), z.o[3]));
     }
   }
 }
@@ -237,24 +268,26 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     kv_attention_kernel(const KvAttentionArgs a) {
   using A = KvAttention<HD, BITS, NG, NT>;
   using F = typename A::F;
-  constexpr int W = A::W, ROWS = A::ROWS, KS = A::KS, MT = A::MT, STAGES = A::STAGES;
+  constexpr int W = A::W, ROWS = A::ROWS, KS = A::KS, MT = A::MT, STAGES = A::STAGES, BP = A::BP;
   constexpr int WORDS = F::LB / 4;              // words of a lane's half
+  constexpr int PW = F::PIECE / 4;              // of a piece
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[W * STAGES];
-  __shared__ int absent[W * STAGES];            // the stage's block has no page
-  __shared__ float q_factor[ROWS];              // t = <row, (c - z) s> * q_factor
-  __shared__ int row_pos[ROWS];
-  __shared__ uint64_t row_mask[ROWS];
-  __shared__ int new_pos[kKvMaxNew];
+  __shared__ __align__(8) uint64_t all_bars[W * STAGES];
+  __shared__ int all_absent[W * STAGES];        // bit u: the stage's block u has no page or is none
   __shared__ float warp_m[W][ROWS], warp_l[W][ROWS];
   __shared__ int abort_flag;
   const KvGeometry& g = a.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, tq = lane & 3;      // row group and quarter of the MMA fragments
-  uint8_t* ring = smem + warp * STAGES * F::BLOCK;
-  uint32_t* qfrag = reinterpret_cast<uint32_t*>(smem + A::UNION);
+  uint8_t* ring = smem + warp * A::WARP_BYTES;
+  uint32_t* qfrag = reinterpret_cast<uint32_t*>(ring + STAGES * A::STAGE);
+  uint64_t* row_mask = reinterpret_cast<uint64_t*>(ring + STAGES * A::STAGE + A::QFRAG);
+  float* q_factor = reinterpret_cast<float*>(row_mask + ROWS);   // t = <row, (c - z) s> * q_factor
+  int* row_pos = reinterpret_cast<int*>(q_factor + ROWS);
+  uint64_t* bars = all_bars + warp * STAGES;
+  int* absent = all_absent + warp * STAGES;
   // {end of its work in blocks of one head (56 bits), n (8 bits); kv; row0}
-  int4* seqs = reinterpret_cast<int4*>(smem + A::UNION + A::QFRAG);
+  int4* seqs = reinterpret_cast<int4*>(smem + A::MAIN);
   auto pack = [](int64_t end, int n, int kv, int row0) {
     return make_int4(static_cast<int>(end), static_cast<int>((end >> 32) & 0xFFFFFF) | n << 24, kv, row0);
   };
@@ -264,10 +297,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 
   allow_dependents_launch();
   if (lane == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&bars[warp * STAGES + s], 1);
-      absent[warp * STAGES + s] = 0;
-    }
+    for (int s = 0; s < STAGES; ++s) mbar_init(&bars[s], 1);
     fence_barrier_init();
   }
   if (tid == 0) abort_flag = 0;
@@ -309,21 +339,22 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
   }
   __syncthreads();
   const int64_t total = g.batch > 0 ? end_of(seqs[g.batch - 1]) * g.kv_heads : 0;
-  // no run shorter than a segment's overhead and 2 blocks a warp, so that short
+  // no run shorter than a segment's overhead and a few blocks, so that short
   // contexts are not cut into pieces whose merge costs more than they do
-  constexpr int LEAST = A::OVERHEAD + 2 * W;
-  const int64_t most = (total + LEAST - 1) / LEAST;
-  const int64_t runs = most < static_cast<int64_t>(gridDim.x) ? most : static_cast<int64_t>(gridDim.x);
-  int4* meta = a.meta + 2 * blockIdx.x;
-  if (tid == 0) meta[0] = make_int4(-1, 0, 0, 0);
-  if (blockIdx.x >= runs) return;
-  int64_t x = blockIdx.x * total / runs;
-  const int64_t x1 = (blockIdx.x + 1) * total / runs;
+  constexpr int LEAST = A::OVERHEAD + 4;
+  const int64_t most = (total + LEAST - 1) / LEAST, all = static_cast<int64_t>(gridDim.x) * W;
+  const int64_t runs = most < all ? most : all;
+  const int64_t run = static_cast<int64_t>(blockIdx.x) * W + warp;
+  int4* meta = a.meta + 2 * run;
+  if (lane == 0) meta[0] = make_int4(-1, 0, 0, 0);
+  // a block's warps all have work or, but for the last, none
+  int64_t x = run < runs ? run * total / runs : 0;
+  const int64_t x1 = run < runs ? (run + 1) * total / runs : 0;
 
   // ---- the segment at x; a segment's blocks follow A::OVERHEAD units of its
   // own cost, so a run that begins within those begins with its first block
-  KvSegment seg;
-  int from, tiles;
+  KvSegment seg = {};
+  int from = 0, count = 0, tiles = 1;
   int64_t left = 0;                             // units of the segment from x on
   auto enter = [&](int b) {                     // sequence b's first segment
     while (((seqs[b].y >> 24) & 0xFF) == 0) ++b;   // there is one: x < total
@@ -333,7 +364,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     seg.blocks = ((seg.kv - 1) >> 4) + 1 - seg.first;
     tiles = tiles_of(seg.n);
   };
-  {
+  if (x < x1) {
     const int64_t per_head_x = x / g.kv_heads;
     int lo = 0, hi = g.batch - 1;               // first b with end * kv_heads > x
     while (lo < hi) {
@@ -347,8 +378,24 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     seg.h = static_cast<int>(tile / tiles);
     seg.tile = static_cast<int>(tile - static_cast<int64_t>(seg.h) * tiles);
   }
+  // whether the whole thread block works on one segment, this run's first:
+  // then its partial results are merged in shared memory
+  const int64_t block_end = (static_cast<int64_t>(blockIdx.x) * W + W) * total / (runs > 0 ? runs : 1);
+  bool together = run < runs && (blockIdx.x + 1) * W <= runs && block_end <= x + left;
+  {
+    const int64_t key = together ? (static_cast<int64_t>(seg.b) << 40 | static_cast<int64_t>(seg.h) << 24 | seg.tile) : -1;
+    __shared__ int64_t keys[W];
+    if (lane == 0) keys[warp] = key;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) together = together && keys[w] == keys[0] && keys[w] >= 0;
+  }
+  if (tid == 0) a.together[blockIdx.x] = together;
+
+  const KvMagic<BITS> magic;
   uint32_t phases = 0;                          // bit s: parity of stage s
-  for (bool started = false; x < x1; started = true) {
+  bool ok = true;
+  for (bool started = false; x < x1 && ok; started = true) {
     if (started && left == 0) {                 // the next segment
       if (++seg.tile == tiles) {
         seg.tile = 0;
@@ -359,208 +406,222 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     // blocks [from, from + count) of it are this run's; none if only a part
     // of its overhead is
     const int64_t take = x1 - x < left ? x1 - x : left;
-    const int end = seg.blocks - static_cast<int>(left - take < seg.blocks ? left - take : seg.blocks);
     from = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks);
-    const int count = end - from;
     x += take;
     left -= take;
-    if (count == 0) continue;
-    const bool whole = from == 0 && count == seg.blocks;
+    count = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks) - from;
+    const bool whole = count == seg.blocks;
     const int old = seg.kv - seg.n;             // positions before the new ones
     const int R = seg.n * a.per, r0 = seg.tile * ROWS;
-    if (started) {
-      // the ring was the merge buffer: order those accesses before the copies
-      fence_proxy_async_smem();
-      __syncthreads();
-    }
+    // (a run of overhead alone goes on below with no blocks: nothing is
+    // stored unless the block merges its warps' results)
+    if (count == 0 && !together) continue;
 
-    // ---- start this warp's copies: blocks from + warp, + W, ...
-    const int mine = count > warp ? (count - warp + W - 1) / W : 0;
-    auto block_of = [&](int i) { return seg.first + from + warp + i * W; };
-    int page_of_lane = -1;                      // page of this warp's block 32 k + lane
-    auto load_pages = [&](int i0) {
-      const int i = i0 + lane;
-      page_of_lane = i < mine ? g.table[seg.b * g.table_stride + block_of(i) / g.page_blocks] : -1;
-    };
-    auto issue = [&](int i) {                   // by the whole warp
-      const int page = __shfl_sync(0xffffffffu, page_of_lane, i & 31);
-      if (lane == 0) {
-        const int s = i % STAGES;
-        uint64_t* bar = &bars[warp * STAGES + s];
-        if (page >= 0 && page < g.num_pages) {
-          const uint8_t* src = g.pages + page * g.page_bytes +
-                               (static_cast<int64_t>(seg.h) * g.page_blocks + block_of(i) % g.page_blocks) * F::BLOCK;
-          absent[warp * STAGES + s] = 0;
-          mbar_arrive_expect_tx(bar, F::BLOCK);
-          bulk_load(smem_addr(ring + s * F::BLOCK), src, F::BLOCK, bar);
-        } else {
-          absent[warp * STAGES + s] = 1;
+    // ---- start the copies, BP blocks a stage
+    const int blk0 = seg.first + from;          // this run's first block of the segment
+    const int steps = (count + BP - 1) / BP;
+    const uint8_t* src = nullptr;               // this lane's block 32 k + lane
+    const uint8_t* src_next = nullptr;
+    auto load_sources = [&](int i0) {
+      const int i = i0 + lane, blk = blk0 + i;
+      src = nullptr;
+      if (i < count) {
+        const int pg = blk / g.page_blocks, page = g.table[seg.b * g.table_stride + pg];
+        if (page >= 0 && page < g.num_pages)
+          src = g.pages + page * g.page_bytes +
+                (static_cast<int64_t>(seg.h) * g.page_blocks + (blk - pg * g.page_blocks)) * F::BLOCK;
+        else
           set_flag(g.status, TTQ_FLAG_BAD_INDEX);
-          mbar_arrive(bar);
+      }
+      if constexpr (BP == 2)
+        src_next = reinterpret_cast<const uint8_t*>(
+            __shfl_down_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), 1));
+    };
+    auto issue = [&](int step) {                // by the whole warp; one lane does it
+      const int i = step * BP, s = step % STAGES;
+      if ((i & 31) == 0) load_sources(i);
+      if (lane == (i & 31)) {
+        const uint32_t dst = smem_addr(ring + s * A::STAGE);
+        if constexpr (BP == 1) {
+          absent[s] = src == nullptr;
+          if (src != nullptr) {
+            mbar_arrive_expect_tx(&bars[s], F::BLOCK);
+            bulk_load(dst, src, F::BLOCK, &bars[s]);
+          } else {
+            mbar_arrive(&bars[s]);
+          }
+        } else {
+          absent[s] = (src == nullptr) | (src_next == nullptr) << 1;
+          if (src != nullptr && src_next == src + F::BLOCK) {
+            mbar_arrive_expect_tx(&bars[s], 2 * F::BLOCK);
+            bulk_load(dst, src, 2 * F::BLOCK, &bars[s]);
+          } else {
+            const uint32_t bytes = (src != nullptr ? F::BLOCK : 0) + (src_next != nullptr ? F::BLOCK : 0);
+            if (bytes != 0) mbar_arrive_expect_tx(&bars[s], bytes);
+            else mbar_arrive(&bars[s]);
+            if (src != nullptr) bulk_load(dst, src, F::BLOCK, &bars[s]);
+            if (src_next != nullptr) bulk_load(dst + F::BLOCK, src_next, F::BLOCK, &bars[s]);
+          }
         }
       }
     };
-    load_pages(0);
     int issued = 0;
-    for (; issued < STAGES && issued < mine; ++issued) issue(issued);
+    for (; issued < STAGES && issued < steps; ++issued) issue(issued);
 
     // ---- the tile's rows of Q as B fragments, and what each row sees
-    {
+    if (count > 0) {
       constexpr int E = HD / 32;                // consecutive channels of a lane
-      constexpr int RW = ROWS / W;              // rows of a warp
-      float v[RW][E];
-#pragma unroll
-      for (int k = 0; k < RW; ++k) {
-        const int rr = r0 + warp * RW + k;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[k][e] = 0.f;
-        if (rr < R) {
-          const int i_new = rr / a.per;
-          kv_load_lane<E>(a.Q, a.q_type,
-                          (seg.row0 + i_new) * a.q_row + (seg.h * a.per + rr - i_new * a.per) * a.q_head + lane * E, v[k]);
-        }
-      }
       float dk[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) dk[e] = a.Dk != nullptr ? __ldg(a.Dk + seg.h * HD + lane * E + e) : 1.f;
 #pragma unroll
-      for (int k = 0; k < RW; ++k) {
-        const int r = warp * RW + k;
-        float big = 0.f;
+      for (int nt = 0; nt < NT; ++nt) {
+        float v[8][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          v[k][e] *= dk[e];
-          big = fmaxf(big, fabsf(v[k][e]));
-        }
-        // the row's largest magnitude: bits of non-negative floats order as integers
-        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-        const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
-        const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^-(ex - 127)
-        const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+        for (int k = 0; k < 8; ++k) {
+          const int rr = r0 + nt * 8 + k;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const int c = lane * E + e, kg = c / F::G, j = c % F::G;
-          const int quarter = j / (F::G / 4), idx = kg * (F::G / 4) + j % (F::G / 4);
-          qfrag[(((r >> 3) * KS + idx / 4) * 32 + 4 * (r & 7) + quarter) * 2 + (idx % 4) / 2] =
-              h2_as_u32(__floats2half2_rn(v[k][e] * down, v[k][e + 1] * down));
+          for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+          if (rr < R) {
+            const int i_new = rr / a.per;
+            kv_load_lane<E>(a.Q, a.q_type,
+                            (seg.row0 + i_new) * a.q_row + (seg.h * a.per + rr - i_new * a.per) * a.q_head + lane * E, v[k]);
+          }
         }
-        if (lane == 0) q_factor[r] = a.scale * up * (a.cap > 0.f ? 1.f / a.cap : kKvLog2e);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = nt * 8 + k;
+          float big = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            v[k][e] *= dk[e];
+            big = fmaxf(big, fabsf(v[k][e]));
+          }
+          // the row's largest magnitude: bits of non-negative floats order as integers
+          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+          const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
+          const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^-(ex - 127)
+          const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const int c = lane * E + e, kg = c / F::G, j = c % F::G;
+            const int quarter = j / (F::G / 4), idx = kg * (F::G / 4) + j % (F::G / 4);
+            qfrag[((nt * KS + idx / 4) * 32 + 4 * k + quarter) * 2 + (idx % 4) / 2] =
+                h2_as_u32(__floats2half2_rn(v[k][e] * down, v[k][e + 1] * down));
+          }
+          if (lane == 0) q_factor[r] = a.scale * up * (a.cap > 0.f ? 1.f / a.cap : kKvLog2e);
+        }
       }
-      if (tid < ROWS) {
-        const int rr = r0 + tid, i_new = rr / a.per;
+      if (lane < ROWS) {
+        const int rr = r0 + lane, i_new = rr / a.per;
         uint64_t mask = 0;
         if (rr < R) mask = a.tree != nullptr ? a.tree[seg.row0 + i_new] : (2ull << i_new) - 1ull;
-        row_mask[tid] = mask;
-        row_pos[tid] = old + __popcll(mask & ~(1ull << (i_new & 63)));
+        row_mask[lane] = mask;
+        row_pos[lane] = old + __popcll(mask & ~(1ull << (i_new & 63)));
       }
-      if (tid >= 64 && tid - 64 < seg.n) {
-        const int i = tid - 64;
-        const uint64_t mask = a.tree != nullptr ? a.tree[seg.row0 + i] : (2ull << i) - 1ull;
-        new_pos[i] = old + __popcll(mask & ~(1ull << i));
-      }
+      __syncwarp();
     }
-    __syncthreads();
 
-    // ---- the loop over this warp's blocks
+    // ---- the loop over this run's blocks
     float o[MT][NT][4] = {};
     float m[NT][2], l[NT][2] = {};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = kKvFloor;
     int e_run = 0;                              // running exponent field of V's scales
-    bool ok = true;
+    // steps [0, plain0) and [plain1, steps) need masks: blocks that the window
+    // of the last new token does not cover, those that reach the new tokens,
+    // and a last step that is not full
+    int plain0 = 0, plain1;
+    {
+      const int64_t past = static_cast<int64_t>(seg.kv) - a.window;   // p >= past is in every row's window
+      if (a.window > 0 && past > 0) {
+        const int64_t need = (past + 15) / 16 - blk0;                 // first block wholly in it
+        plain0 = need <= 0 ? 0 : need >= count ? steps : static_cast<int>((need + BP - 1) / BP);
+      }
+      const int full = (old >> 4) - blk0;                             // blocks before the new tokens
+      plain1 = (full < 0 ? 0 : full < count ? full : count) / BP;
+    }
 
-    auto process = [&](auto masked_c, uint32_t st, int blk, bool gone) {
+    auto process = [&](auto masked_c, uint32_t st, int blk, int gone) {
       constexpr bool MASKED = decltype(masked_c)::value;
       // -- scores
-      float s[NT][4];
+      float s[BP][NT][4];
+      uint32_t kp[BP][2][NG];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-      uint32_t kw[2][WORDS];
-      kv_lane_words<F::LB, F::PIECE>(st, lane, 0, kw[0]);
-      kv_lane_words<F::LB, F::PIECE>(st, lane, 1, kw[1]);
-      uint32_t kp[2][NG];
-      kv_lds<NG>(st + F::CODES + gr * NG * 4, kp[0]);
-      kv_lds<NG>(st + F::CODES + (gr + 8) * NG * 4, kp[1]);
+      for (int u = 0; u < BP; ++u) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
+        kv_lds<NG>(st + u * F::BLOCK + F::CODES + gr * NG * 4, kp[u][0]);
+        kv_lds<NG>(st + u * F::BLOCK + F::CODES + (gr + 8) * NG * 4, kp[u][1]);
+      }
       constexpr int KSG = KS / NG;              // k steps of a group
       constexpr int KSW = BITS == 8 ? 1 : 32 / BITS / 4;   // k steps of a word
-      uint32_t pa[2][2 * KSW];
+      uint32_t kw[BP][2][PW], pa[BP][2][2 * KSW];
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
-        float acc[NT][4];
+        float acc[BP][NT][4];
+        KvZero<BITS> z[BP][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-        KvZero<BITS> z[2];
+        for (int u = 0; u < BP; ++u) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) z[r].set(__byte_perm(kp[r][k], 0, 0x3232));
+          for (int nt = 0; nt < NT; ++nt) acc[u][nt][0] = acc[u][nt][1] = acc[u][nt][2] = acc[u][nt][3] = 0.f;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) z[u][r].set(__byte_perm(kp[u][r][k], 0, 0x3232));
+        }
 #pragma unroll
         for (int j = 0; j < KSG; ++j) {
           const int ks = k * KSG + j, w = ks / KSW, in = ks % KSW;
-          if (in == 0 || j == 0) {
+#pragma unroll
+          for (int u = 0; u < BP; ++u)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              if constexpr (BITS == 8) {
-                kv_e4m3x4(kw[r][w], pa[r][0], pa[r][1]);
-              } else {
-                kv_int_pairs<BITS>(kw[r][w], z[r], pa[r]);
+              if (in == 0 && w % PW == 0)
+                kv_lds<PW>(st + u * F::BLOCK + (w / PW * 2 + r) * 32 * F::PIECE + lane * F::PIECE, kw[u][r]);
+              if (in == 0 || j == 0) {
+                if constexpr (BITS == 8) kv_e4m3x4(kw[u][r][w % PW], pa[u][r][0], pa[u][r][1]);
+                else kv_int_pairs<BITS>(kw[u][r][w % PW], z[u][r], magic, pa[u][r]);
               }
             }
-          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * KS + ks) * 32 + lane) * 2);
-            kv_mma(acc[nt], pa[0][2 * in], pa[1][2 * in], pa[0][2 * in + 1], pa[1][2 * in + 1], bq.x, bq.y);
+#pragma unroll
+            for (int u = 0; u < BP; ++u)
+              kv_mma(acc[u][nt], pa[u][0][2 * in], pa[u][1][2 * in], pa[u][0][2 * in + 1], pa[u][1][2 * in + 1], bq.x, bq.y);
           }
         }
-        const float s0 = __half2float(u32_as_h2(kp[0][k]).x), s1 = __half2float(u32_as_h2(kp[1][k]).x);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          s[nt][0] = fmaf(acc[nt][0], s0, s[nt][0]);
-          s[nt][1] = fmaf(acc[nt][1], s0, s[nt][1]);
-          s[nt][2] = fmaf(acc[nt][2], s1, s[nt][2]);
-          s[nt][3] = fmaf(acc[nt][3], s1, s[nt][3]);
-        }
-      }
-      // -- V's words; of a block that is not all there, tokens that are not are zeroed
-      uint32_t vw[2][WORDS];
-      kv_lane_words<F::LB, F::PIECE>(st + F::V_OFFSET, lane, 0, vw[0]);
-      kv_lane_words<F::LB, F::PIECE>(st + F::V_OFFSET, lane, 1, vw[1]);
-      uint32_t vp[2][NG], vz[2][NG];            // (s, z) of tokens gr, gr + 8; zeros of 2 tq, 2 tq + 1 (+ 8)
-      const uint32_t vpairs = st + F::V_OFFSET + F::CODES;
-      kv_lds<NG>(vpairs + gr * NG * 4, vp[0]);
-      kv_lds<NG>(vpairs + (gr + 8) * NG * 4, vp[1]);
+        for (int u = 0; u < BP; ++u) {
+          const float s0 = __half2float(u32_as_h2(kp[u][0][k]).x), s1 = __half2float(u32_as_h2(kp[u][1][k]).x);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t e0[NG], e1[NG];
-        kv_lds<NG>(vpairs + (2 * tq + 8 * r) * NG * 4, e0);
-        kv_lds<NG>(vpairs + (2 * tq + 1 + 8 * r) * NG * 4, e1);
-#pragma unroll
-        for (int k = 0; k < NG; ++k) vz[r][k] = __byte_perm(e0[k], e1[k], 0x7632);
-      }
-      const int there = MASKED ? (gone ? 0 : seg.kv - blk * 16) : 16;   // tokens of the block
-      if constexpr (MASKED) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int t0 = 2 * tq + 8 * r;
-          const uint32_t keep = (t0 < there ? 0xFFFFu : 0u) | (t0 + 1 < there ? 0xFFFF0000u : 0u);
-#pragma unroll
-          for (int w = 0; w < WORDS; ++w) vw[r][w] &= keep;
-#pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            vz[r][k] &= keep;
-            if (gr + 8 * r >= there) vp[r][k] = 0;
+          for (int nt = 0; nt < NT; ++nt) {
+            s[u][nt][0] = fmaf(acc[u][nt][0], s0, s[u][nt][0]);
+            s[u][nt][1] = fmaf(acc[u][nt][1], s0, s[u][nt][1]);
+            s[u][nt][2] = fmaf(acc[u][nt][2], s1, s[u][nt][2]);
+            s[u][nt][3] = fmaf(acc[u][nt][3], s1, s[u][nt][3]);
           }
         }
       }
-      // -- the largest finite scale's exponent, over all of the block's V
+      // -- V's pairs of tokens gr and gr + 8, and the largest finite scale's
+      // exponent over all of V; tokens that are not there count for nothing
+      int there[BP];                            // tokens of the block
+      uint32_t vp[BP][2][NG];
       {
         uint32_t sb = 0;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int u = 0; u < BP; ++u) {
+          there[u] = MASKED ? ((gone >> u & 1) ? 0 : seg.kv - (blk + u) * 16) : 16;
 #pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            const uint32_t bits = vp[r][k] & 0x7FFFu;
-            sb = max(sb, bits < 0x7C00u ? bits : 0u);
+          for (int r = 0; r < 2; ++r) {
+            kv_lds<NG>(st + u * F::BLOCK + F::V_OFFSET + F::CODES + (gr + 8 * r) * NG * 4, vp[u][r]);
+#pragma unroll
+            for (int k = 0; k < NG; ++k) {
+              if (MASKED && gr + 8 * r >= there[u]) vp[u][r][k] = 0;
+              const uint32_t bits = vp[u][r][k] & 0x7FFFu;
+              sb = max(sb, bits < 0x7C00u ? bits : 0u);
+            }
           }
+        }
         const int e_new = static_cast<int>(__reduce_max_sync(0xffffffffu, sb) >> 10);
         if (e_new > e_run) {
           const float f = __uint_as_float(static_cast<uint32_t>(127 + e_run - e_new) << 23);
@@ -577,40 +638,58 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       bool higher = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float f0 = q_factor[8 * nt + 2 * tq], f1 = q_factor[8 * nt + 2 * tq + 1];
+        const float2 f = *reinterpret_cast<const float2*>(q_factor + 8 * nt + 2 * tq);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float t = s[nt][i] * ((i & 1) ? f1 : f0);
-          if (a.cap > 0.f)    // cap tanh(t) = cap (1 - 2 / (1 + e^{2 t}))
-            t = a.cap * kKvLog2e * (1.f - 2.f * kv_rcp(1.f + kv_exp2(t * (2.f * kKvLog2e))));
-          if constexpr (MASKED) {
-            const int j = (i & 2) ? gr + 8 : gr, p = blk * 16 + j, row = 8 * nt + 2 * tq + (i & 1);
-            bool see = j < there;
-            if (see && p >= old) {
-              see = (row_mask[row] >> (p - old)) & 1ull;
-              if (a.window > 0) see = see && row_pos[row] - new_pos[p - old] < a.window;
-            } else if (see && a.window > 0) {
-              see = row_pos[row] - p < a.window;
-            }
-            t = see ? t : -INFINITY;
-          }
-          s[nt][i] = t;
-          higher |= t > m[nt][i & 1] + kKvSlack;
-        }
+        for (int u = 0; u < BP; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[u][nt][i] *= (i & 1) ? f.y : f.x;
       }
+      if (a.cap > 0.f) {      // cap tanh(t) = cap (1 - 2 / (1 + e^{2 t}))
+#pragma unroll
+        for (int u = 0; u < BP; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              s[u][nt][i] = a.cap * kKvLog2e * (1.f - 2.f * kv_rcp(1.f + kv_exp2(s[u][nt][i] * (2.f * kKvLog2e))));
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < BP; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (MASKED) {
+              const int j = (i & 2) ? gr + 8 : gr, p = (blk + u) * 16 + j, row = 8 * nt + 2 * tq + (i & 1);
+              bool see = j < there[u];
+              if (see && p >= old) {
+                see = (row_mask[row] >> (p - old)) & 1ull;
+                if (see && a.window > 0) {
+                  const int k_new = p - old;
+                  const uint64_t mask = a.tree != nullptr ? a.tree[seg.row0 + k_new] : (2ull << k_new) - 1ull;
+                  see = row_pos[row] - old - __popcll(mask & ~(1ull << k_new)) < a.window;
+                }
+              } else if (see && a.window > 0) {
+                see = row_pos[row] - p < a.window;
+              }
+              if (!see) s[u][nt][i] = -INFINITY;
+            }
+            higher |= s[u][nt][i] > m[nt][i & 1] + kKvSlack;
+          }
       // -- the running maximum moves only when a score is well above it
       if (__any_sync(0xffffffffu, higher)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(s[nt][c], s[nt][c + 2]);
+            float mx = m[nt][c];
+#pragma unroll
+            for (int u = 0; u < BP; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][c], s[u][nt][c + 2]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m_new = fmaxf(m[nt][c], mx);
-            const float f = kv_exp2(m[nt][c] - m_new);
-            m[nt][c] = m_new;
+            const float f = kv_exp2(m[nt][c] - mx);
+            m[nt][c] = mx;
             l[nt][c] *= f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -622,93 +701,116 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[nt][i] = kv_exp2(s[nt][i] - m[nt][i & 1]);
-          l[nt][i & 1] += s[nt][i];
-        }
+        for (int u = 0; u < BP; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[u][nt][i] = kv_exp2(s[u][nt][i] - m[nt][i & 1]);
+            l[nt][i & 1] += s[u][nt][i];
+          }
       // -- p s_V 2^-E as the B operand, and the second product
       const float vf = __uint_as_float(static_cast<uint32_t>(127 + 14 - e_run) << 23);   // s 2^(14 - e) < 1
       constexpr int MTG = MT / NG;              // m tiles of a group
       constexpr int MTW = BITS == 8 ? 1 : 16 / BITS / 2;   // m tiles of a word
-      uint32_t pv[2][BITS == 8 ? 2 : 16 / BITS];
 #pragma unroll
-      for (int k = 0; k < NG; ++k) {
-        const float s0 = __half2float(u32_as_h2(vp[0][k]).x) * vf, s1 = __half2float(u32_as_h2(vp[1][k]).x) * vf;
-        uint32_t b[NT][2];
+      for (int u = 0; u < BP; ++u) {
+        const uint32_t vst = st + u * F::BLOCK + F::V_OFFSET;
+        uint32_t vz[2][NG], keep[2] = {};       // zeros of tokens 2 tq, 2 tq + 1 (+ 8)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float w0 = s[nt][0] * s0, w1 = s[nt][1] * s0, w2 = s[nt][2] * s1, w3 = s[nt][3] * s1;
-          if constexpr (MASKED) {               // a NaN scale reaches only those that see its token
-            w0 = s[nt][0] == 0.f ? 0.f : w0;
-            w1 = s[nt][1] == 0.f ? 0.f : w1;
-            w2 = s[nt][2] == 0.f ? 0.f : w2;
-            w3 = s[nt][3] == 0.f ? 0.f : w3;
+        for (int r = 0; r < 2; ++r) {
+          if constexpr (MASKED) {
+            const int t0 = 2 * tq + 8 * r;
+            keep[r] = (t0 < there[u] ? 0xFFFFu : 0u) | (t0 + 1 < there[u] ? 0xFFFF0000u : 0u);
           }
-          b[nt][0] = kv_transpose(h2_as_u32(__floats2half2_rn(w0, w1)));
-          b[nt][1] = kv_transpose(h2_as_u32(__floats2half2_rn(w2, w3)));
-        }
-        KvZero<BITS> z[2];
+          if constexpr (BITS != 8) {
+            uint32_t e0[NG], e1[NG];
+            kv_lds<NG>(vst + F::CODES + (2 * tq + 8 * r) * NG * 4, e0);
+            kv_lds<NG>(vst + F::CODES + (2 * tq + 1 + 8 * r) * NG * 4, e1);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) z[r].set(vz[r][k]);
-#pragma unroll
-        for (int j = 0; j < MTG; ++j) {
-          const int mt = k * MTG + j, w = mt / MTW, in = mt % MTW;
-          if (in == 0 || j == 0) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              if constexpr (BITS == 8) {        // bytes: even token's two channels, then the odd one's
-                kv_e4m3x4(__byte_perm(vw[r][w], 0, 0x3120), pv[r][0], pv[r][1]);
-              } else {
-                kv_int_pairs<BITS>(vw[r][w], z[r], pv[r]);
-              }
+            for (int k = 0; k < NG; ++k) {
+              vz[r][k] = __byte_perm(e0[k], e1[k], 0x7632);
+              if constexpr (MASKED) vz[r][k] &= keep[r];
             }
           }
+        }
+        uint32_t vw[2][PW], pv[2][BITS == 8 ? 2 : 16 / BITS];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            kv_mma(o[mt][nt], pv[0][2 * in], pv[0][2 * in + 1], pv[1][2 * in], pv[1][2 * in + 1], b[nt][0], b[nt][1]);
+        for (int k = 0; k < NG; ++k) {
+          const float s0 = __half2float(u32_as_h2(vp[u][0][k]).x) * vf, s1 = __half2float(u32_as_h2(vp[u][1][k]).x) * vf;
+          uint32_t b[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float w0 = s[u][nt][0] * s0, w1 = s[u][nt][1] * s0, w2 = s[u][nt][2] * s1, w3 = s[u][nt][3] * s1;
+            if constexpr (MASKED) {             // a NaN scale reaches only those that see its token
+              w0 = s[u][nt][0] == 0.f ? 0.f : w0;
+              w1 = s[u][nt][1] == 0.f ? 0.f : w1;
+              w2 = s[u][nt][2] == 0.f ? 0.f : w2;
+              w3 = s[u][nt][3] == 0.f ? 0.f : w3;
+            }
+            b[nt][0] = kv_transpose(h2_as_u32(__floats2half2_rn(w0, w1)));
+            b[nt][1] = kv_transpose(h2_as_u32(__floats2half2_rn(w2, w3)));
+          }
+          KvZero<BITS> z[2];
+          if constexpr (BITS != 8) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) z[r].set(vz[r][k]);
+          }
+#pragma unroll
+          for (int j = 0; j < MTG; ++j) {
+            const int mt = k * MTG + j, w = mt / MTW, in = mt % MTW;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if (in == 0 && w % PW == 0) {
+                kv_lds<PW>(vst + (w / PW * 2 + r) * 32 * F::PIECE + lane * F::PIECE, vw[r]);
+                if constexpr (MASKED) {
+#pragma unroll
+                  for (int i = 0; i < PW; ++i) vw[r][i] &= keep[r];
+                }
+              }
+              if (in == 0 || j == 0) {
+                if constexpr (BITS == 8)        // bytes: even token's two channels, then the odd one's
+                  kv_e4m3x4(__byte_perm(vw[r][w % PW], 0, 0x3120), pv[r][0], pv[r][1]);
+                else
+                  kv_int_pairs<BITS>(vw[r][w % PW], z[r], magic, pv[r]);
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              kv_mma(o[mt][nt], pv[0][2 * in], pv[0][2 * in + 1], pv[1][2 * in], pv[1][2 * in + 1], b[nt][0], b[nt][1]);
+          }
         }
       }
     };
 
     int done = 0;
-    for (; done < mine; ++done) {
-      const int i = done, s = i % STAGES;
-      if (!mbar_wait(&bars[warp * STAGES + s], (phases >> s) & 1u, &abort_flag)) {
+    for (; done < steps; ++done) {
+      const int s = done % STAGES;
+      if (!mbar_wait(&bars[s], (phases >> s) & 1u, &abort_flag)) {
         ok = false;
         break;
       }
       phases ^= 1u << s;
-      const int blk = block_of(i);
-      const bool gone = absent[warp * STAGES + s] != 0;
-      const uint32_t st = smem_addr(ring + s * F::BLOCK);
-      // masks matter in blocks that reach the new tokens, or that the window
-      // of the last new token does not cover
-      const bool masked = gone || blk * 16 + 16 > old ||
-                          (a.window > 0 && blk * 16 <= static_cast<int64_t>(seg.kv) - 1 - a.window);
-      if (masked) process(std::true_type{}, st, blk, gone);
-      else process(std::false_type{}, st, blk, false);
+      const int gone = absent[s];
+      const uint32_t st = smem_addr(ring + s * A::STAGE);
+      if (gone != 0 || done < plain0 || done >= plain1) process(std::true_type{}, st, blk0 + done * BP, gone);
+      else process(std::false_type{}, st, blk0 + done * BP, 0);
       __syncwarp();
-      if (issued < mine) {
-        if ((issued & 31) == 0) load_pages(issued);
-        issue(issued);
-        ++issued;
-      }
+      if (issued < steps) issue(issued++);
     }
     if (!ok) {
       // a copy did not arrive in time: say so and wait, with the same limit,
-      // for the copies still in flight
+      // for the copies still in flight; the run ends here
       if (lane == 0) {
         set_flag(g.status, TTQ_FLAG_TIMEOUT);
         abort_flag = 1;
         for (int i = done; i < issued; ++i) {
           int never = 0;
-          mbar_wait(&bars[warp * STAGES + i % STAGES], (phases >> (i % STAGES)) & 1u, &never);
+          mbar_wait(&bars[i % STAGES], (phases >> (i % STAGES)) & 1u, &never);
         }
       }
       __syncwarp();
     }
 
-    // ---- merge the warps' states
+    // ---- the end of the segment, or of this run's part of it
     const float back = __uint_as_float(static_cast<uint32_t>(127 + e_run - 14) << 23);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -718,123 +820,167 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         v += __shfl_xor_sync(0xffffffffu, v, 4);
         v += __shfl_xor_sync(0xffffffffu, v, 8);
         v += __shfl_xor_sync(0xffffffffu, v, 16);
-        if (gr == 0) {
-          warp_m[warp][8 * nt + 2 * tq + c] = m[nt][c];
-          warp_l[warp][8 * nt + 2 * tq + c] = v;
-        }
+        l[nt][c] = v;
       }
-    __syncthreads();                            // every warp is done with the ring
-    const bool failed = *static_cast<volatile int*>(&abort_flag) != 0;
-    float* buf = reinterpret_cast<float*>(smem);
+    // the four channels of m tiles mt and mt + 1 that this lane holds of a row
+    auto channel = [&](int mt) { return 2 * mt / (F::G / 8) * F::G + gr * (F::G / 8) + 2 * mt % (F::G / 8); };
+    auto four = [&](int mt, int nt, int c) {
+      return make_float4(o[mt][nt][c] * back, o[mt][nt][c + 2] * back, o[mt + 1][nt][c] * back, o[mt + 1][nt][c + 2] * back);
+    };
+    if (together) {
+      __syncthreads();                          // every warp is done with its ring
+      float* buf = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          const int r = 8 * nt + 2 * tq + c;
+          if (gr == 0) {
+            warp_m[warp][r] = m[nt][c];
+            warp_l[warp][r] = l[nt][c];
+          }
 #pragma unroll
-        for (int mt = 0; mt < MT; mt += 2) {
-          // channels of this lane: 2 mt, 2 mt + 1, 2 mt + 2, 2 mt + 3 of its stream
-          const int k = 2 * mt / (F::G / 8), j = 2 * mt % (F::G / 8);
-          const int ch = k * F::G + gr * (F::G / 8) + j;
-          *reinterpret_cast<float4*>(buf + (warp * ROWS + 8 * nt + 2 * tq + c) * A::LDO + ch) =
-              make_float4(o[mt][nt][c] * back, o[mt][nt][c + 2] * back, o[mt + 1][nt][c] * back,
-                          o[mt + 1][nt][c + 2] * back);
+          for (int mt = 0; mt < MT; mt += 2)
+            *reinterpret_cast<float4*>(buf + (warp * ROWS + r) * A::LDO + channel(mt)) = four(mt, nt, c);
         }
-    __syncthreads();
-    // this run's slot of the workspace: the first if the segment began in an
-    // earlier run
-    float* slot = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (from > 0 ? 0 : 1)) * A::SLOT;
-    for (int i = tid; i < ROWS * (HD / 4); i += W * 32) {
-      const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
-      if (r0 + r >= R) continue;
-      float mx = warp_m[0][r];
+      __syncthreads();
+      // the block's results go to its first warp's slot; the block has the
+      // whole segment if its runs do
+      const int64_t first_run = static_cast<int64_t>(blockIdx.x) * W;
+      float* slot = a.part + 2 * first_run * A::SLOT;
+      for (int i = tid; i < ROWS * (HD / 4); i += W * 32) {
+        const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
+        if (r0 + r >= R) continue;
+        float mx = warp_m[0][r];
 #pragma unroll
-      for (int w = 1; w < W; ++w) mx = fmaxf(mx, warp_m[w][r]);
-      float sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 1; w < W; ++w) mx = fmaxf(mx, warp_m[w][r]);
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float f = kv_exp2(warp_m[w][r] - mx);
-        const float4 v = *reinterpret_cast<const float4*>(buf + (w * ROWS + r) * A::LDO + ch);
-        sum = fmaf(warp_l[w][r], f, sum);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
-      }
-      if (whole) {
-        kv_store_row<HD>(a, seg.row0, seg.h, r0 + r, ch, acc, sum);
-      } else {
+        for (int w = 0; w < W; ++w) {
+          const float f = kv_exp2(warp_m[w][r] - mx);
+          const float4 v = *reinterpret_cast<const float4*>(buf + (w * ROWS + r) * A::LDO + ch);
+          sum = fmaf(warp_l[w][r], f, sum);
+          acc.x = fmaf(v.x, f, acc.x);
+          acc.y = fmaf(v.y, f, acc.y);
+          acc.z = fmaf(v.z, f, acc.z);
+          acc.w = fmaf(v.w, f, acc.w);
+        }
         *reinterpret_cast<float4*>(slot + r * HD + ch) = acc;
         if (ch == 0) {
           slot[ROWS * HD + r] = mx;
           slot[ROWS * HD + ROWS + r] = sum;
         }
       }
+    } else if (whole) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = r0 + 8 * nt + 2 * tq + c;
+          if (r < R) {
+#pragma unroll
+            for (int mt = 0; mt < MT; mt += 2) kv_store_row<HD>(a, seg.row0, seg.h, r, channel(mt), four(mt, nt, c), l[nt][c]);
+          }
+        }
+    } else {
+      // the run's first slot if the segment began in an earlier run
+      float* slot = a.part + (2 * run + (from > 0 ? 0 : 1)) * A::SLOT;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = 8 * nt + 2 * tq + c;
+          if (r0 + r < R) {
+#pragma unroll
+            for (int mt = 0; mt < MT; mt += 2)
+              *reinterpret_cast<float4*>(slot + r * HD + channel(mt)) = four(mt, nt, c);
+            if (gr == 0) {
+              slot[ROWS * HD + r] = m[nt][c];
+              slot[ROWS * HD + ROWS + r] = l[nt][c];
+            }
+          }
+        }
     }
-    if (tid == 0 && from == 0 && !whole) {
+    if (lane == 0 && from == 0 && count > 0 && !whole) {
       // the run that holds the segment's last block: the last i with i total / runs <= its place
       const int64_t last = x + left - 1;
       meta[0] = make_int4(static_cast<int>(((last + 1) * runs - 1) / total), seg.row0, seg.h, r0);
       meta[1] = make_int4(R, 0, 0, 0);
     }
-    if (failed) return;      // the same for all threads: set before the barriers above
   }
 }
 
-// Merges the partial results of the segment that began in run blockIdx.x and
-// went on into later runs: a block takes one row, its threads are the float4
-// channels of the row times slices of the partial results, which are
-// summed per slice and then over the slices, always in the same order.
+// Merges the partial results of the segments that began in the runs of
+// thread block blockIdx.x and went on into later runs.  A block takes one
+// row of each; its threads are the float4 channels of the row times slices
+// of the contributing thread blocks, summed per slice and then over the
+// slices, always in the same order.
 constexpr int kKvJoinThreads = 256;
-template <int HD, int ROWS>
+template <int HD, int ROWS, int W>
 __global__ void __launch_bounds__(kKvJoinThreads) kv_join_kernel(const KvAttentionArgs a) {
   constexpr int SLOT = ROWS * (HD + 2), LANES = HD / 4, SLICES = kKvJoinThreads / LANES;
   __shared__ float4 acc_s[SLICES][LANES];
-  __shared__ float sum_s[SLICES];
+  __shared__ float sum_s[SLICES], max_s[SLICES];
   allow_dependents_launch();
   grid_dependency_wait();
-  const int4 m0 = a.meta[2 * blockIdx.x];
-  if (m0.x < 0) return;
-  const int R = a.meta[2 * blockIdx.x + 1].x;
-  const int first = blockIdx.x, last = m0.x, row0 = m0.y, h = m0.z, r0 = m0.w, r = blockIdx.y;
-  if (r0 + r >= R) return;
-  const int slice = threadIdx.x / LANES, ch = (threadIdx.x % LANES) * 4;
-  // partial result k of the segment is in the first slot of run first + k, but for k = 0
-  auto slot_of = [&](int k) { return a.part + (2 * static_cast<int64_t>(first + k) + (k == 0 ? 1 : 0)) * SLOT; };
-  const int n = last - first + 1;
-  float mx = kKvFloor;
-  for (int k = threadIdx.x; k < n; k += kKvJoinThreads) mx = fmaxf(mx, slot_of(k)[ROWS * HD + r]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  __shared__ float max_s[kKvJoinThreads / 32];
-  if (threadIdx.x % 32 == 0) max_s[threadIdx.x / 32] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kKvJoinThreads / 32; ++w) mx = fmaxf(mx, max_s[w]);
-  float sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int slice = threadIdx.x / LANES, in = threadIdx.x % LANES, ch = in * 4, r = blockIdx.y;
+  for (int w = 0; w < W; ++w) {
+    const int first = blockIdx.x * W + w;
+    const int4 m0 = a.meta[2 * first];
+    if (m0.x < 0) continue;
+    const int R = a.meta[2 * first + 1].x;
+    const int last = m0.x, row0 = m0.y, h = m0.z, r0 = m0.w;
+    if (r0 + r >= R) continue;
+    float mx = kKvFloor, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float* slot) {
+      const float4 v = *reinterpret_cast<const float4*>(slot + r * HD + ch);
+      const float mk = slot[ROWS * HD + r], lk = slot[ROWS * HD + ROWS + r];
+      const float m_new = fmaxf(mx, mk);
+      const float f = kv_exp2(mx - m_new), fk = kv_exp2(mk - m_new);
+      mx = m_new;
+      sum = fmaf(lk, fk, sum * f);
+      acc.x = fmaf(v.x, fk, acc.x * f);
+      acc.y = fmaf(v.y, fk, acc.y * f);
+      acc.z = fmaf(v.z, fk, acc.z * f);
+      acc.w = fmaf(v.w, fk, acc.w * f);
+    };
 #pragma unroll 4
-  for (int k = slice; k < n; k += SLICES) {
-    const float* slot = slot_of(k);
-    const float4 v = *reinterpret_cast<const float4*>(slot + r * HD + ch);
-    const float f = kv_exp2(slot[ROWS * HD + r] - mx);
-    sum = fmaf(slot[ROWS * HD + ROWS + r], f, sum);
-    acc.x = fmaf(v.x, f, acc.x);
-    acc.y = fmaf(v.y, f, acc.y);
-    acc.z = fmaf(v.z, f, acc.z);
-    acc.w = fmaf(v.w, f, acc.w);
-  }
-  acc_s[slice][threadIdx.x % LANES] = acc;
-  if (ch == 0) sum_s[slice] = sum;
-  __syncthreads();
-  if (slice != 0) return;
+    for (int k = first / W + slice; k <= last / W; k += SLICES) {
+      if (a.together[k]) {
+        add(a.part + 2 * static_cast<int64_t>(k) * W * SLOT);
+      } else {
+        const int lo = max(first, k * W), hi = min(last, k * W + W - 1);
+        for (int q = lo; q <= hi; ++q) add(a.part + (2 * static_cast<int64_t>(q) + (q == first ? 1 : 0)) * SLOT);
+      }
+    }
+    acc_s[slice][in] = acc;
+    if (in == 0) {
+      sum_s[slice] = sum;
+      max_s[slice] = mx;
+    }
+    __syncthreads();
+    if (slice == 0) {
+      float top = max_s[0];
 #pragma unroll
-  for (int w = 1; w < SLICES; ++w) {
-    const float4 v = acc_s[w][threadIdx.x];
-    sum += sum_s[w];
-    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      for (int k = 1; k < SLICES; ++k) top = fmaxf(top, max_s[k]);
+      sum = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < SLICES; ++k) {
+        const float f = kv_exp2(max_s[k] - top);
+        const float4 v = acc_s[k][in];
+        sum = fmaf(sum_s[k], f, sum);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+      kv_store_row<HD>(a, row0, h, r0 + r, ch, acc, sum);
+    }
+    __syncthreads();
   }
-  kv_store_row<HD>(a, row0, h, r0 + r, ch, acc, sum);
 }
 
 // One head size's kernels (a source file each).
@@ -899,7 +1045,7 @@ cudaError_t kv_attention_launch(const KvAttentionArgs& a, int bits, int group, c
     }
     e = launch_kernel(kernel, dim3(p.grid), dim3(A::W * 32), smem, stream, true, a);
     if (e != cudaSuccess) return;
-    e = launch_kernel(kv_join_kernel<HD, A::ROWS>, dim3(p.grid, A::ROWS), dim3(kKvJoinThreads), 0, stream, true, a);
+    e = launch_kernel(kv_join_kernel<HD, A::ROWS, A::W>, dim3(p.grid, A::ROWS), dim3(kKvJoinThreads), 0, stream, true, a);
   });
   return e;
 }

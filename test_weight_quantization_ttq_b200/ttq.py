@@ -225,6 +225,17 @@ def _stream(stream) -> int | None:
     return s.cuda_stream or None
 
 
+# the current stream's handle without building a torch.cuda.Stream (which
+# costs 3 us, as much as a launch), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, device: int) -> int | None:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device) or None
+    return _stream(stream)
+
+
 # ------------------------------------------------------------- workspace
 def ttq_workspace_size(d, dp, T, r, bits, group, dtype=TTQ_BF16) -> int:
     return int(lib().ttq_workspace_size(d, dp, T, r, bits, group, dtype))
@@ -657,25 +668,35 @@ def _rows_of(t: torch.Tensor, name: str, rows: int, heads, head_dim: int) -> Non
     """t is [rows][heads][head_dim] with contiguous channels (heads None: any number)."""
     if t.dtype not in _ROW_TYPES:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {list(_ROW_TYPES)}")
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, '*' if heads is None else heads, head_dim)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != head_dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(rows, '*' if heads is None else heads, head_dim)}")
     if t.stride(2) != 1:
         raise ValueError(f"the channels of {name} must be contiguous, got strides {t.stride()}")
 
 
-def _strided(t: torch.Tensor, name: str) -> tuple:
-    """(pointer, row stride, head stride) of a row tensor on the current device."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    cur = torch.cuda.current_device()
-    if t.device.index != cur:
-        raise ValueError(f"{name} is on {t.device}; the library runs on the current device cuda:{cur}")
+def _strided(t: torch.Tensor, name: str, device: int) -> tuple:
+    """(pointer, row stride, head stride) of a row tensor on this device."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{device}, got {t.device}")
+    (rows, heads, _), (row, head, _), at = t.shape, t.stride(), t.data_ptr()
     # the stride of a size that is not walked along says nothing
-    row, head = t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
-    if row % 8 or head % 8 or t.data_ptr() % 16:
+    row, head = row if rows > 1 else 0, head if heads > 1 else 0
+    if row % 8 or head % 8 or at % 16:
         raise ValueError(f"the rows of {name} must be 16-byte aligned: strides {t.stride()} are not multiples of 8 "
                          "elements, or its first element is not at a 16-byte boundary")
-    return t.data_ptr(), row, head
+    return at, row, head
+
+
+def _on(t: torch.Tensor | None, name: str, device: int) -> int | None:
+    """Pointer of a contiguous tensor on this device (None stays None)."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -707,16 +728,17 @@ class KVCache:
         self._struct = None
 
     def _arg(self):
+        """(the C struct, its device), which is the current one."""
         if self._struct is None:
             self._struct = _CacheStruct(_dev(self.pages, "pages"), self.pages.shape[0], self.page_size, self.kv_heads,
                                         self.head_dim, self.bits, self.group, self.scheme, _dev(self.D_k, "D_k"),
                                         _dev(self.D_v, "D_v"), _dev(self.D_k_rsqrt, "D_k_rsqrt"),
                                         _dev(self.D_v_rsqrt, "D_v_rsqrt"))
-            self._ref = ctypes.byref(self._struct)
-        elif self.pages.device.index != torch.cuda.current_device():
+            self._ref, self._device = ctypes.byref(self._struct), self.pages.get_device()
+        elif self._device != torch.cuda.current_device():
             raise ValueError(f"pages is on {self.pages.device}; the library runs on the current device "
                              f"cuda:{torch.cuda.current_device()}")
-        return self._ref
+        return self._ref, self._device
 
 
 class KVBatch:
@@ -734,14 +756,14 @@ class KVBatch:
         self.page_table, self.kv_len, self.cu_new, self.rows, self.max_new = page_table, kv_len, cu_new, rows, max_new
         self._struct = None
 
-    def _arg(self, cache):
+    def _arg(self, device):
         if self._struct is None:
-            self._struct = _BatchStruct(_dev(self.page_table, "page_table"), self.page_table.shape[1],
-                                        _dev(self.kv_len, "kv_len"), _dev(self.cu_new, "cu_new"), self.kv_len.shape[0],
-                                        self.rows, self.max_new)
-            self._ref = ctypes.byref(self._struct)
-        if self.kv_len.device != cache.pages.device:
-            raise ValueError(f"the batch is on {self.kv_len.device}, the cache on {cache.pages.device}")
+            self._struct = _BatchStruct(_on(self.page_table, "page_table", device), self.page_table.shape[1],
+                                        _on(self.kv_len, "kv_len", device), _on(self.cu_new, "cu_new", device),
+                                        self.kv_len.shape[0], self.rows, self.max_new)
+            self._ref, self._device = ctypes.byref(self._struct), device
+        if self._device != device:
+            raise ValueError(f"the batch is on {self.kv_len.device}, the cache on cuda:{device}")
         return self._ref
 
 
@@ -785,13 +807,12 @@ def ttq_kv_write(cache, batch, K, V, ws=None, stream=None) -> None:
     _rows_of(V, "V", batch.rows, cache.kv_heads, cache.head_dim)
     if K.dtype != V.dtype:
         raise TypeError(f"K and V have different dtypes {K.dtype} and {V.dtype}")
-    rows = (*_strided(K, "K"), *_strided(V, "V"))
-    c = cache._arg()
-    b = batch._arg(cache)
+    c, device = cache._arg()
+    b = batch._arg(device)
     if ws is None:
         ws = new_kv_workspace(cache, batch, None, stream)
-    _check(lib().ttq_kv_write(c, b, *rows, _dtype_code(K), _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
-           "ttq_kv_write")
+    _check(lib().ttq_kv_write(c, b, *_strided(K, "K", device), *_strided(V, "V", device), _dtype_code(K),
+                              _on(ws, "ws", device), _nbytes(ws), _stream_on(stream, device)), "ttq_kv_write")
 
 
 def ttq_kv_read(cache, batch, K=None, V=None, dtype=None, ws=None, stream=None):
@@ -806,17 +827,17 @@ def ttq_kv_read(cache, batch, K=None, V=None, dtype=None, ws=None, stream=None):
     dtype = dtype or torch.bfloat16
     if dtype not in _ROW_TYPES:
         raise TypeError(f"unsupported dtype {dtype} (float32, bfloat16 or float16)")
-    c = cache._arg()
-    b = batch._arg(cache)
+    c, device = cache._arg()
+    b = batch._arg(device)
     shape = (batch.rows, cache.kv_heads, cache.head_dim)
     if K is None:
         K = _empty(shape, dtype, cache.pages.device, stream)
     if V is None:
-        V = _empty(shape, dtype, cache.pages.device, stream)
+        V = torch.empty_like(K) if stream is None else _empty(shape, dtype, cache.pages.device, stream)
     if ws is None:
         ws = new_kv_workspace(cache, batch, None, stream)
-    _check(lib().ttq_kv_read(c, b, _dev(K, "K"), _dev(V, "V"), _dtype_code(K), _dev(ws, "ws"), _nbytes(ws),
-                             _stream(stream)), "ttq_kv_read")
+    _check(lib().ttq_kv_read(c, b, _on(K, "K", device), _on(V, "V", device), _dtype_code(K), _on(ws, "ws", device),
+                             _nbytes(ws), _stream_on(stream, device)), "ttq_kv_read")
     return K, V
 
 
@@ -841,14 +862,17 @@ def ttq_kv_attention(cache, batch, Q, scale, softcap=0.0, window=0, tree=None, w
     y_dtype = Y.dtype if Y is not None else (y_dtype or Q.dtype)
     if y_dtype not in _ROW_TYPES:
         raise TypeError(f"unsupported dtype {y_dtype} (float32, bfloat16 or float16)")
-    q = _strided(Q, "Q")
-    c = cache._arg()
-    b = batch._arg(cache)
+    c, device = cache._arg()
+    b = batch._arg(device)
+    q = _strided(Q, "Q", device)
     if Y is None:
-        Y = _empty(Q.shape, y_dtype, Q.device, stream)
+        if stream is None and y_dtype == Q.dtype and Q.is_contiguous():
+            Y = torch.empty_like(Q)
+        else:
+            Y = _empty(Q.shape, y_dtype, Q.device, stream)
     if ws is None:
         ws = new_kv_workspace(cache, batch, heads, stream)
-    _check(lib().ttq_kv_attention(c, b, *q, _dtype_code(Q), heads, scale, softcap, window, _dev(tree, "tree"),
-                                  _dev(Y, "Y"), _dtype_code(Y), _dev(ws, "ws"), _nbytes(ws), _stream(stream)),
-           "ttq_kv_attention")
+    _check(lib().ttq_kv_attention(c, b, *q, _dtype_code(Q), heads, scale, softcap, window, _on(tree, "tree", device),
+                                  _on(Y, "Y", device), _dtype_code(Y), _on(ws, "ws", device), _nbytes(ws),
+                                  _stream_on(stream, device)), "ttq_kv_attention")
     return Y

@@ -88,7 +88,7 @@ def test_read(hd, bits, group, page, dtype, stat):
     # one of the two alone, through the C ABI
     L = ttq.lib()
     only = old.clone()
-    assert L.ttq_kv_read(cache._arg(), batch._arg(cache), None, only.data_ptr(), ttq._dtype_code(only), ws.data_ptr(),
+    assert L.ttq_kv_read(cache._arg()[0], batch._arg(0), None, only.data_ptr(), ttq._dtype_code(only), ws.data_ptr(),
                          ws.numel(), torch.cuda.current_stream().cuda_stream) == ttq.TTQ_OK
     assert torch.equal(only, got[1])
 
