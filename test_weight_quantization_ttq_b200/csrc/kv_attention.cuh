@@ -17,15 +17,22 @@
 // A warp brings its blocks through a ring of shared memory stages by bulk
 // copies (codes and pairs of K and V of a block are contiguous), BP blocks a
 // stage.  Products are m16n8k16 with the codes as the A operand:
-//   S^T [16 tokens x 8 rows] = (c - z)_K Q^T   per group of channels, then
-//       scaled by the token's s_K in fp32;
+//   S^T [16 tokens x 8 rows] = (c - z)_K Q^T   per group of channels, scaled
+//       by the token's s_K in fp32;
 //   O^T [channels x 8 rows] += (c - z)_V^T (p s_V)^T.
-// c - z is exact in binary16 and is formed in two instructions per pair of
-// codes: the code bits are put under an exponent whose unit they count
-// (1024 + c, 256 + c, 64 + c or 16 + c by their place in the word), and that
-// offset + z is subtracted.  p s_V moves from the accumulator layout (tokens
-// along the lanes' rows) to the B operand's by an 8 x 8 transposition within
-// the warp.
+// An INT field's code c is taken where it stands: masked out of its word and
+// put under an exponent whose unit it counts, it reads as 1024 + c, 256 + c,
+// 64 + c or 16 + c, and those above 64 are brought down to 64 or 16 (exact).
+// The offsets and zeros are taken off the sums instead of every element:
+// S - sum(offset q) - z sum(q) with the sums of q formed once per segment,
+// and for the second product sum(p s (offset + z)), one more accumulator per
+// group with offset + z as the operand.  (Codes read as subnormals would
+// need neither offset nor exponent, but the matrix instruction aligns its
+// sums by the operands' exponents and keeps some 8 bits less of those: errors
+// of 2^-15 of the raw sums, measured.)  With more than 8 rows those
+// accumulators would not fit the registers; there V's operand is c - z itself.
+// p s_V moves from the accumulator layout (tokens along the lanes' rows) to
+// the B operand's by an 8 x 8 transposition within the warp.
 //
 // Numerics.  Each row of q (times D_k^{-1/2}) is scaled by a power of two to
 // [1, 2) and rounded to binary16.  Scores, the running maximum m and the sum
@@ -55,7 +62,11 @@ struct KvAttention {
   static constexpr int KS = HD / 16;                // k steps of the first product
   static constexpr int MT = HD / 16;                // m tiles of the second
   static constexpr int QFRAG = NT * KS * 32 * 8;    // a warp's Q fragments
-  static constexpr int ROWINFO = ROWS * 16;         // and what it knows of its rows
+  static constexpr int ROWINFO = ROWS * (16 + 8 * NG);   // and what it knows of its rows
+  // whether V's codes are taken raw and their zeros off the sums (see above)
+  static constexpr bool VRAW = BITS != 8 && NT == 1 && NG <= 2;
+  // what even and odd fields of a half word are offset by
+  static constexpr uint32_t EVEN = 0x54005400u, ODD = BITS == 4 ? 0x54005400u : 0x4C004C00u;   // 64; 64 or 16
   // Blocks of threads per SM: by registers 4 where a thread's HD NT / 4
   // accumulators are at most 32 (128 registers), 3 for 64 (168), else 2; fewer
   // where their rings would not have two stages.  A stage holds 2 blocks of
@@ -81,12 +92,12 @@ struct KvAttention {
   static constexpr int SLOT = ROWS * (HD + 2);      // floats of a partial result
   // what a segment costs besides its blocks, in blocks: its rows of Q, the
   // first copy's latency and its end
-  static constexpr int OVERHEAD = 2;
+  static constexpr int OVERHEAD = 4;
 };
 
 __device__ __forceinline__ void kv_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                        uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -194,6 +205,25 @@ __device__ __forceinline__ void kv_int_pairs(uint32_t w, const KvZero<BITS>& z, 
   }
 }
 
+// The offset pairs of a word: p[i] holds the i-th field of the low and of
+// the high half, plus 64 (even fields) or 64 / 16 (odd fields of INT4 / INT2).
+template <int BITS>
+__device__ __forceinline__ void kv_offset_pairs(uint32_t w, const KvMagic<BITS>& c, uint32_t* p) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = i ? w >> 8 : w;
+    if constexpr (BITS == 4) {
+      p[2 * i] = h2_as_u32(__hadd2(kv_field<0x000F000Fu>(u, c.v[0]), u32_as_h2(0xE380E380u)));       // 1024 - 960
+      p[2 * i + 1] = h2_as_u32(kv_field<0x00F000F0u>(u, c.v[1]));
+    } else {
+      p[4 * i] = h2_as_u32(__hadd2(kv_field<0x00030003u>(u, c.v[0]), u32_as_h2(0xE380E380u)));       // 1024 - 960
+      p[4 * i + 1] = h2_as_u32(__hadd2(kv_field<0x000C000Cu>(u, c.v[2]), u32_as_h2(0xDB80DB80u)));   // 256 - 240
+      p[4 * i + 2] = h2_as_u32(kv_field<0x00300030u>(u, c.v[1]));
+      p[4 * i + 3] = h2_as_u32(kv_field<0x00C000C0u>(u, c.v[3]));
+    }
+  }
+}
+
 struct KvSegment {
   int b, h, tile;        // sequence, key/value head, tile of rows
   int row0, n, kv;       // the sequence's first row, its rows and positions
@@ -284,6 +314,8 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
   uint64_t* row_mask = reinterpret_cast<uint64_t*>(ring + STAGES * A::STAGE + A::QFRAG);
   float* q_factor = reinterpret_cast<float*>(row_mask + ROWS);   // t = <row, (c - z) s> * q_factor
   int* row_pos = reinterpret_cast<int*>(q_factor + ROWS);
+  float* q_sum = reinterpret_cast<float*>(row_pos + ROWS);       // [NG][ROWS] sums of a row's group
+  float* q_off = q_sum + NG * ROWS;                              // the same with the fields' offsets as weights
   uint64_t* bars = all_bars + warp * STAGES;
   int* absent = all_absent + warp * STAGES;
   // {end of its work in blocks of one head (56 bits), n (8 bits); kv; row0}
@@ -520,6 +552,27 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         row_pos[lane] = old + __popcll(mask & ~(1ull << (i_new & 63)));
       }
       __syncwarp();
+      if constexpr (BITS != 8) {
+        // the sums of each group of the rounded rows: the first product with
+        // ones, and with the offsets, as codes
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float one[4] = {}, off[4] = {};
+#pragma unroll
+            for (int j = 0; j < KS / NG; ++j) {
+              const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * KS + k * (KS / NG) + j) * 32 + lane) * 2);
+              kv_mma(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, bq.x, bq.y);
+              kv_mma(off, A::EVEN, A::EVEN, A::ODD, A::ODD, bq.x, bq.y);
+            }
+            if (gr == 0) {
+              *reinterpret_cast<float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq) = make_float2(one[0], one[1]);
+              *reinterpret_cast<float2*>(q_off + k * ROWS + 8 * nt + 2 * tq) = make_float2(off[0], off[1]);
+            }
+          }
+        __syncwarp();
+      }
     }
 
     // ---- the loop over this run's blocks
@@ -527,7 +580,20 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     float m[NT][2], l[NT][2] = {};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = kKvFloor;
-    int e_run = 0;                              // running exponent field of V's scales
+    int e_run = 0;                              // running exponent field of V's scales (binary32's; 0: none yet)
+    float zs[A::VRAW ? NG : 1][4] = {};         // sums of p s (offset + z) 2^-E per group
+    // takes the offsets and zeros off the accumulators, often enough that the
+    // sums of offset codes do not grow much past their difference
+    auto centre = [&]() {
+      if constexpr (A::VRAW) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[mt][0][i] -= zs[mt / (MT / NG)][i];
+#pragma unroll
+        for (int k = 0; k < NG; ++k) zs[k][0] = zs[k][1] = zs[k][2] = zs[k][3] = 0.f;
+      }
+    };
     // steps [0, plain0) and [plain1, steps) need masks: blocks that the window
     // of the last new token does not cover, those that reach the new tokens,
     // and a last step that is not full
@@ -560,14 +626,10 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
         float acc[BP][NT][4];
-        KvZero<BITS> z[BP][2];
 #pragma unroll
-        for (int u = 0; u < BP; ++u) {
+        for (int u = 0; u < BP; ++u)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) acc[u][nt][0] = acc[u][nt][1] = acc[u][nt][2] = acc[u][nt][3] = 0.f;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) z[u][r].set(__byte_perm(kp[u][r][k], 0, 0x3232));
-        }
 #pragma unroll
         for (int j = 0; j < KSG; ++j) {
           const int ks = k * KSG + j, w = ks / KSW, in = ks % KSW;
@@ -577,9 +639,9 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
             for (int r = 0; r < 2; ++r) {
               if (in == 0 && w % PW == 0)
                 kv_lds<PW>(st + u * F::BLOCK + (w / PW * 2 + r) * 32 * F::PIECE + lane * F::PIECE, kw[u][r]);
-              if (in == 0 || j == 0) {
+              if (in == 0) {
                 if constexpr (BITS == 8) kv_e4m3x4(kw[u][r][w % PW], pa[u][r][0], pa[u][r][1]);
-                else kv_int_pairs<BITS>(kw[u][r][w % PW], z[u][r], magic, pa[u][r]);
+                else kv_offset_pairs<BITS>(kw[u][r][w % PW], magic, pa[u][r]);
               }
             }
 #pragma unroll
@@ -592,9 +654,18 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         }
 #pragma unroll
         for (int u = 0; u < BP; ++u) {
-          const float s0 = __half2float(u32_as_h2(kp[u][0][k]).x), s1 = __half2float(u32_as_h2(kp[u][1][k]).x);
+          const float2 p0 = __half22float2(u32_as_h2(kp[u][0][k])), p1 = __half22float2(u32_as_h2(kp[u][1][k]));
+          const float s0 = p0.x, s1 = p1.x;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (BITS != 8) {
+              const float2 qs = *reinterpret_cast<const float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq);
+              const float2 qo = *reinterpret_cast<const float2*>(q_off + k * ROWS + 8 * nt + 2 * tq);
+              acc[u][nt][0] = fmaf(-p0.y, qs.x, acc[u][nt][0] - qo.x);
+              acc[u][nt][1] = fmaf(-p0.y, qs.y, acc[u][nt][1] - qo.y);
+              acc[u][nt][2] = fmaf(-p1.y, qs.x, acc[u][nt][2] - qo.x);
+              acc[u][nt][3] = fmaf(-p1.y, qs.y, acc[u][nt][3] - qo.y);
+            }
             s[u][nt][0] = fmaf(acc[u][nt][0], s0, s[u][nt][0]);
             s[u][nt][1] = fmaf(acc[u][nt][1], s0, s[u][nt][1]);
             s[u][nt][2] = fmaf(acc[u][nt][2], s1, s[u][nt][2]);
@@ -602,35 +673,42 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           }
         }
       }
-      // -- V's pairs of tokens gr and gr + 8, and the largest finite scale's
-      // exponent over all of V; tokens that are not there count for nothing
+      // -- V's scales of tokens gr and gr + 8, and the exponent of the largest
+      // over all of V (NaN aside); tokens that are not there count for nothing
       int there[BP];                            // tokens of the block
-      uint32_t vp[BP][2][NG];
+      float vs[BP][2][NG];
       {
-        uint32_t sb = 0;
+        float top = 0.f;
 #pragma unroll
         for (int u = 0; u < BP; ++u) {
           there[u] = MASKED ? ((gone >> u & 1) ? 0 : seg.kv - (blk + u) * 16) : 16;
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            kv_lds<NG>(st + u * F::BLOCK + F::V_OFFSET + F::CODES + (gr + 8 * r) * NG * 4, vp[u][r]);
+            uint32_t vp[NG];
+            kv_lds<NG>(st + u * F::BLOCK + F::V_OFFSET + F::CODES + (gr + 8 * r) * NG * 4, vp);
 #pragma unroll
             for (int k = 0; k < NG; ++k) {
-              if (MASKED && gr + 8 * r >= there[u]) vp[u][r][k] = 0;
-              const uint32_t bits = vp[u][r][k] & 0x7FFFu;
-              sb = max(sb, bits < 0x7C00u ? bits : 0u);
+              vs[u][r][k] = __half2float(u32_as_h2(vp[k]).x);
+              if (MASKED && gr + 8 * r >= there[u]) vs[u][r][k] = 0.f;
+              top = fmaxf(top, vs[u][r][k]);
             }
           }
         }
-        const int e_new = static_cast<int>(__reduce_max_sync(0xffffffffu, sb) >> 10);
+        const int e_new = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23);
         if (e_new > e_run) {
-          const float f = __uint_as_float(static_cast<uint32_t>(127 + e_run - e_new) << 23);
+          const float f = e_run == 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + e_run - e_new) << 23);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f;
+          if constexpr (A::VRAW) {
+#pragma unroll
+            for (int k = 0; k < NG; ++k)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) zs[k][i] *= f;
+          }
           e_run = e_new;
         }
       }
@@ -696,6 +774,13 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
               o[mt][nt][c] *= f;
               o[mt][nt][c + 2] *= f;
             }
+            if constexpr (A::VRAW) {
+#pragma unroll
+              for (int k = 0; k < NG; ++k) {
+                zs[k][c] *= f;
+                zs[k][c + 2] *= f;
+              }
+            }
           }
       }
 #pragma unroll
@@ -708,13 +793,13 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
             l[nt][i & 1] += s[u][nt][i];
           }
       // -- p s_V 2^-E as the B operand, and the second product
-      const float vf = __uint_as_float(static_cast<uint32_t>(127 + 14 - e_run) << 23);   // s 2^(14 - e) < 1
+      const float vf = __uint_as_float(static_cast<uint32_t>(253 - (e_run == 0 ? 126 : e_run)) << 23);   // s vf < 1
       constexpr int MTG = MT / NG;              // m tiles of a group
       constexpr int MTW = BITS == 8 ? 1 : 16 / BITS / 2;   // m tiles of a word
 #pragma unroll
       for (int u = 0; u < BP; ++u) {
         const uint32_t vst = st + u * F::BLOCK + F::V_OFFSET;
-        uint32_t vz[2][NG], keep[2] = {};       // zeros of tokens 2 tq, 2 tq + 1 (+ 8)
+        [[maybe_unused]] uint32_t vz[2][NG], keep[2] = {};   // zeros of tokens 2 tq, 2 tq + 1 (+ 8)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if constexpr (MASKED) {
@@ -735,7 +820,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         uint32_t vw[2][PW], pv[2][BITS == 8 ? 2 : 16 / BITS];
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-          const float s0 = __half2float(u32_as_h2(vp[u][0][k]).x) * vf, s1 = __half2float(u32_as_h2(vp[u][1][k]).x) * vf;
+          const float s0 = vs[u][0][k] * vf, s1 = vs[u][1][k] * vf;
           uint32_t b[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -749,8 +834,19 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
             b[nt][0] = kv_transpose(h2_as_u32(__floats2half2_rn(w0, w1)));
             b[nt][1] = kv_transpose(h2_as_u32(__floats2half2_rn(w2, w3)));
           }
-          KvZero<BITS> z[2];
-          if constexpr (BITS != 8) {
+          [[maybe_unused]] KvZero<BITS> z[2];
+          if constexpr (A::VRAW) {
+            // rows of even fields, then of odd ones
+            const uint32_t e0 = h2_as_u32(__hadd2(u32_as_h2(vz[0][k]), u32_as_h2(A::EVEN)));
+            const uint32_t e1 = h2_as_u32(__hadd2(u32_as_h2(vz[1][k]), u32_as_h2(A::EVEN)));
+            if constexpr (BITS == 4) {
+              kv_mma(zs[k], e0, e0, e1, e1, b[0][0], b[0][1]);
+            } else {
+              const uint32_t d0 = h2_as_u32(__hadd2(u32_as_h2(vz[0][k]), u32_as_h2(A::ODD)));
+              const uint32_t d1 = h2_as_u32(__hadd2(u32_as_h2(vz[1][k]), u32_as_h2(A::ODD)));
+              kv_mma(zs[k], e0, d0, e1, d1, b[0][0], b[0][1]);
+            }
+          } else if constexpr (BITS != 8) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) z[r].set(vz[r][k]);
           }
@@ -766,9 +862,11 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
                   for (int i = 0; i < PW; ++i) vw[r][i] &= keep[r];
                 }
               }
-              if (in == 0 || j == 0) {
+              if (in == 0 || (!A::VRAW && j == 0)) {
                 if constexpr (BITS == 8)        // bytes: even token's two channels, then the odd one's
                   kv_e4m3x4(__byte_perm(vw[r][w % PW], 0, 0x3120), pv[r][0], pv[r][1]);
+                else if constexpr (A::VRAW)
+                  kv_offset_pairs<BITS>(vw[r][w % PW], magic, pv[r]);
                 else
                   kv_int_pairs<BITS>(vw[r][w % PW], z[r], magic, pv[r]);
               }
@@ -795,7 +893,9 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       else process(std::false_type{}, st, blk0 + done * BP, 0);
       __syncwarp();
       if (issued < steps) issue(issued++);
+      if ((done & 15) == 15) centre();
     }
+    centre();
     if (!ok) {
       // a copy did not arrive in time: say so and wait, with the same limit,
       // for the copies still in flight; the run ends here
@@ -811,7 +911,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     }
 
     // ---- the end of the segment, or of this run's part of it
-    const float back = __uint_as_float(static_cast<uint32_t>(127 + e_run - 14) << 23);
+    const float back = __uint_as_float(static_cast<uint32_t>(e_run == 0 ? 127 : e_run + 1) << 23);   // 1 / vf
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -116,6 +116,18 @@ def quantise(cache, rows: np.ndarray, D=None):
     return q, s, z
 
 
+def magnitudes(cache, codes, scales, zeros, Dr=None) -> np.ndarray:
+    """float64 s (64 + max(q, z)) [D^{-1/2}] (s |q| for E4M3): what the sums of offset codes and of offset zeros
+    are made of."""
+    if cache.bits == 8:
+        return np.abs(values(cache, codes, scales, zeros, Dr))
+    s = np.ascontiguousarray(scales).view(np.float16).astype(np.float64)
+    z = np.ascontiguousarray(zeros).view(np.float16).astype(np.float64)
+    q = codes.astype(np.float64).reshape(*codes.shape[:-1], -1, cache.group)
+    v = ((64 + np.maximum(q, z[..., None])) * s[..., None]).reshape(codes.shape)
+    return v if Dr is None else v * Dr.astype(np.float64)[:, None, :]
+
+
 class Case:
     """A cache with random contents, and a batch with the given new rows and
     lengths.  Tokens behind a sequence's length are left as random bytes."""
@@ -168,15 +180,15 @@ class Case:
                             max(self.new + [0]))
         return cache, batch
 
-    def sequence(self, b: int, pages: np.ndarray | None = None, Dr=(None, None)):
-        """K and V of sequence b, float64 [heads][kv][hd]."""
+    def sequence(self, b: int, pages: np.ndarray | None = None, Dr=(None, None), of=values):
+        """K and V (or another function `of` their codes) of sequence b, float64 [heads][kv][hd]."""
         pages = self.host if pages is None else pages
         n, page = self.kv[b], self.cache.page_size
         own = self.table[b, :-(-n // page)]
         out = []
         for which, (q, s, z) in enumerate(unpack(pages[own], self.cache)):
             join = lambda a: a.transpose(1, 0, 2, 3).reshape(a.shape[1], -1, a.shape[3])[:, :n]
-            out.append(values(self.cache, join(q), join(s), join(z), Dr[which]))
+            out.append(of(self.cache, join(q), join(s), join(z), Dr[which]))
         return out
 
 
@@ -195,20 +207,26 @@ def visible(n: int, kv: int, window: int = 0, masks=None) -> np.ndarray:
     return out
 
 
-def attention(K, V, Q, scale, see, cap=0.0, q_rounded=False, smax=None, code_max=15.0):
+def attention(K, V, Q, scale, see, cap=0.0, q_rounded=False, smax=None, code_max=15.0, raw=None):
     """(y, bound) for one sequence: K, V float64 [heads][kv][hd], Q float64
-    [n][query heads][hd], see [n][kv].  The bound on the kernel's error, from
-    its own roundings:
-      scores: the products' fp32 sums, hd terms at 2^-23 each of the sum of
-        magnitudes, 8 roundings of the score itself at 2^-23, and Q rounded to
-        binary16 (2^-11 each) where it is (q_rounded);
+    [n][query heads][hd], see [n][kv]; raw: (K, V) of magnitudes().  The bound
+    on the kernel's error, from its own roundings:
+      scores: the fp32 sums of q times offset codes, offsets and zeros, hd / 16
+        matrix instructions and two more terms at 2^-22 each of the sum of
+        magnitudes (truncated sums: a whole unit 2^-23, twice), 8 roundings of
+        the score itself at 2^-23, and Q rounded to binary16 (2^-11 each) where
+        it is (q_rounded), else 2^-20 of the row's largest for the elements
+        that are subnormal beside it;
       probabilities: a relative 2 d for a score error of d, 2^-20 for the
         exponentials and the sums' fp32 roundings;
       p s_V rounded to binary16: 2^-11 relative, or 2^-25 in units of at
-        most twice the largest scale where it is subnormal."""
+        most twice the largest scale where it is subnormal;
+      the second product: at most 34 truncated additions of offset codes between
+        two times that offsets and zeros are taken off, 2^-23 each."""
     n, hq, hd = Q.shape
     heads, kv = K.shape[:2]
     per = hq // heads
+    K_raw, V_raw = raw if raw is not None else (np.abs(K), np.abs(V))
     y, bound = np.zeros((n, hq, hd)), np.zeros((n, hq, hd))
     for h in range(hq):
         k, v = K[h // per], V[h // per]
@@ -219,7 +237,10 @@ def attention(K, V, Q, scale, see, cap=0.0, q_rounded=False, smax=None, code_max
             q = Q[i, h]
             t = scale * (k[js] @ q)
             mag = abs(scale) * (np.abs(k[js]) @ np.abs(q))
-            d = mag * hd * 2.0 ** -23 + np.abs(t) * 8 * 2.0 ** -23 + (mag * 2.0 ** -11 if q_rounded else 0.0)
+            mag_raw = abs(scale) * (K_raw[h // per][js] @ np.abs(q))
+            top = abs(scale) * np.abs(k[js]).sum(-1) * np.abs(q).max()
+            d = mag_raw * (hd / 16 + 2) * 2.0 ** -22 + np.abs(t) * 8 * 2.0 ** -23
+            d = d + (mag * 2.0 ** -11 if q_rounded else 0.0) + top * 2.0 ** -20
             if cap > 0:
                 t = cap * np.tanh(t / cap)
                 d = d + cap * 2.0 ** -20
@@ -227,8 +248,8 @@ def attention(K, V, Q, scale, see, cap=0.0, q_rounded=False, smax=None, code_max
             weight = p.sum()       # at most the kernel's: its maximum is never above the largest score
             p /= weight
             y[i, h] = p @ v[js]
-            a = p @ np.abs(v[js])
-            bound[i, h] = a * (2 * d.max() + 2.0 ** -20 + 2.0 ** -11 + js.size * 2.0 ** -24)
+            a, a_raw = p @ np.abs(v[js]), p @ V_raw[h // per][js]
+            bound[i, h] = a * (2 * d.max() + 2.0 ** -20 + 2.0 ** -11 + js.size * 2.0 ** -24) + a_raw * 34 * 2.0 ** -23
             if smax is not None:
                 bound[i, h] += js.size * 2.0 ** -25 * 2 * smax * code_max / weight
     return y, bound

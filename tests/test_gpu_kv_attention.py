@@ -59,13 +59,15 @@ def check(case, per=4, dtype=bf16, y_dtype=None, cap=0.0, window=0, masks=None, 
             smax *= float(case.Dr[1].max())
         y, bound = R.attention(K, V, Q[r].double().numpy(), float(np.float32(scale)), see, cap,
                                q_rounded=dtype == f32 or case.Dr[0] is not None, smax=smax,
-                               code_max=448.0 if f.bits == 8 else 2.0 ** f.bits - 1)
+                               code_max=448.0 if f.bits == 8 else 2.0 ** f.bits - 1,
+                               raw=case.sequence(b, Dr=case.Dr, of=R.magnitudes))
         tol = bound + (np.abs(y) + bound) * R.HALF_STEP[Y.dtype] + 2.0 ** -24
         bad = ~(np.abs(got[r] - y) <= tol)
         assert not bad.any(), (b, int(bad.sum()), float(np.nanmax(np.abs(got[r] - y) / tol)))
         # and the bound says something: it is well below the values.  Where Q is rounded it holds twice the worst case
         # 2^-11 scale sum |k q| of a score, some 27 / 2^10 of p |V| at q_scale 3, and p |V| is several times |y|.
-        part = 0.25 if dtype == f32 or case.Dr[0] is not None else 0.1
+        # (INT2: a score also holds twice 2^-22 (hd / 16 + 2) scale sum |q| s (64 + 3).)
+        part = 0.25 if dtype == f32 or case.Dr[0] is not None or f.bits == 2 else 0.1
         assert bound.mean() <= part * np.sqrt(np.mean(y ** 2)) + 1e-4, (bound.mean(), np.sqrt(np.mean(y ** 2)))
     return Y
 
