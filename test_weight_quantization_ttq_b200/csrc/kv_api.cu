@@ -10,7 +10,12 @@ namespace ttq {
 namespace {
 
 constexpr size_t kStatusBytes = 4096;     // the least workspace an entry point takes
-constexpr size_t kKvHeader = 4096;        // the attention's regions start here
+// The part of a workspace that ttq_workspace_init zeroes and every call leaves
+// at zero: the status word, then the attention's tickets from byte 256.
+constexpr size_t kKvHeader = 20480;
+constexpr size_t kKvTickets = 256;
+static_assert(kKvTickets + 2 * 4 * kKvPlanSMs * kKvAttentionWarps * sizeof(uint32_t) <= kKvHeader,
+              "two tickets a warp, of at most 4 blocks per SM");
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -95,11 +100,8 @@ KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows
                    : hd == 128 ? kv_attention_ctas_hd128(bits, group, p.nt)
                                : kv_attention_ctas_hd256(bits, group, p.nt);
   p.grid = ctas * kKvPlanSMs;
-  p.slot_floats = static_cast<int64_t>(8 * p.nt) * (hd + 2);
-  const int64_t warps = static_cast<int64_t>(p.grid) * kKvAttentionWarps;
-  p.meta_bytes = warps * 2 * sizeof(int4);
-  p.together_bytes = (p.grid * 4 + 255) / 256 * 256;
-  p.part_bytes = warps * 2 * p.slot_floats * 4;
+  p.slot_floats = static_cast<int64_t>(8 * p.nt) * (hd + 4);
+  p.part_bytes = static_cast<int64_t>(p.grid) * kKvAttentionWarps * 2 * p.slot_floats * 4;
   return p;
 }
 
@@ -158,7 +160,7 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
   if (max_new < 0 || max_new > kKvMaxNew) return 0;
   const KvAttentionPlan p = kv_attention_plan(head_dim, bits, group, max_new * (heads / kv_heads));
   if (p.grid == 0) return 0;
-  return kKvHeader + p.meta_bytes + p.together_bytes + p.part_bytes;
+  return kKvHeader + p.part_bytes;
 }
 
 ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch, const void* Q,
@@ -194,9 +196,8 @@ ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch
   a.window = window;
   a.tree = tree;
   a.Y = Y;
-  a.meta = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kKvHeader);
-  a.together = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kKvHeader + p.meta_bytes);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kKvHeader + p.meta_bytes + p.together_bytes);
+  a.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kKvTickets);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kKvHeader);
   return status_of(launch_kv_attention(a, cache->head_dim, cache->bits, cache->group, p,
                                        static_cast<cudaStream_t>(stream)));
 }

@@ -9,14 +9,16 @@
 // tile) with all blocks of 16 tokens that it may see.  All segments'
 // blocks, laid end to end, are cut into equal runs, one per warp of the
 // grid, so that contexts of any lengths load the SMs evenly and no warp
-// waits for another; a segment cut by a run's end leaves partial results
-// (running maximum, sum and accumulator) in the workspace, which
-// kv_join_kernel merges in a fixed order.  Where all warps of a thread block
-// work on one segment, they merge theirs first.
+// waits for another.  A warp whose run ends inside a segment leaves a partial
+// result (running maximum, sum and accumulator) in the workspace; the warp
+// whose ticket is the last of the segment's merges them in their order, so
+// that the result does not depend on who is last.  Where all warps of a
+// thread block work on one segment they merge theirs first, and where there
+// are many results groups of them are merged before the whole.
 //
 // A warp brings its blocks through a ring of shared memory stages by bulk
-// copies (codes and pairs of K and V of a block are contiguous), BP blocks a
-// stage.  Products are m16n8k16 with the codes as the A operand:
+// copies, one per block (codes and pairs of K and V are contiguous).
+// Products are m16n8k16 with the codes as the A operand:
 //   S^T [16 tokens x 8 rows] = (c - z)_K Q^T   per group of channels, scaled
 //       by the token's s_K in fp32;
 //   O^T [channels x 8 rows] += (c - z)_V^T (p s_V)^T.
@@ -38,8 +40,8 @@
 // [1, 2) and rounded to binary16.  Scores, the running maximum m and the sum
 // l are fp32.  m moves only when a score exceeds it by more than 8 (in
 // powers of two), which keeps p <= 256; p s_V is rounded to binary16 after
-// scaling by 2^-E, E the running maximum of the exponents of s_V, so that
-// scales of any size use binary16's normal range.
+// scaling by 2^-E, 2^E a scale of V that no scale so far exceeds more than 64
+// times, so that scales of any size use binary16's normal range.
 #pragma once
 
 #include <atomic>
@@ -62,37 +64,34 @@ struct KvAttention {
   static constexpr int KS = HD / 16;                // k steps of the first product
   static constexpr int MT = HD / 16;                // m tiles of the second
   static constexpr int QFRAG = NT * KS * 32 * 8;    // a warp's Q fragments
-  static constexpr int ROWINFO = ROWS * (16 + 8 * NG);   // and what it knows of its rows
+  static constexpr int ROWINFO = ROWS * (24 + 8 * NG);   // and what it knows of its rows
   // whether V's codes are taken raw and their zeros off the sums (see above)
   static constexpr bool VRAW = BITS != 8 && NT == 1 && NG <= 2;
   // what even and odd fields of a half word are offset by
   static constexpr uint32_t EVEN = 0x54005400u, ODD = BITS == 4 ? 0x54005400u : 0x4C004C00u;   // 64; 64 or 16
   // Blocks of threads per SM: by registers 4 where a thread's HD NT / 4
   // accumulators are at most 32 (128 registers), 3 for 64 (168), else 2; fewer
-  // where their rings would not have two stages.  A stage holds 2 blocks of
-  // tokens, so that its wait, vote and masks are paid once, where the scores
-  // of 32 tokens fit those registers (NT = 1) and two such stages the memory.
+  // where their rings would not have two stages.
   static constexpr int SM_BYTES = 212 * 1024;
   static constexpr int room(int ctas) { return SM_BYTES / (ctas * W) - QFRAG - ROWINFO - 512; }
   static constexpr int BY_REGS = HD * NT / 4 <= 32 ? 4 : HD * NT / 4 <= 64 ? 3 : 2;
   static constexpr int CTAS = BY_REGS >= 4 && room(4) >= 2 * F::BLOCK ? 4 : BY_REGS >= 3 && room(3) >= 2 * F::BLOCK ? 3 : 2;
-  static constexpr int BP = NT == 1 && room(CTAS) >= 4 * F::BLOCK ? 2 : 1;
-  static constexpr int warp_room = room(CTAS);
-  static constexpr int STAGES_FIT = warp_room / (BP * F::BLOCK);
-  static constexpr int STAGES = STAGES_FIT > 4 ? 4 : STAGES_FIT;
-  static_assert(STAGES >= 2, "the ring needs two stages");
-  static constexpr int STAGE = BP * F::BLOCK;
-  static constexpr int WARP_BYTES = STAGES * STAGE + QFRAG + ROWINFO;
+  static constexpr int STAGES = room(CTAS) >= 4 * F::BLOCK ? 4 : 2;
+  static_assert(room(CTAS) >= 2 * F::BLOCK, "the ring needs two stages");
+  static constexpr int WARP_BYTES = STAGES * F::BLOCK + QFRAG + ROWINFO;
   static constexpr int LDO = HD + 4;                // padded row of the merge buffer
   static constexpr int MERGE = W * ROWS * LDO * 4;
-  static constexpr int MAIN = W * WARP_BYTES > MERGE ? W * WARP_BYTES : MERGE;
   // dynamic shared memory: the warps' regions (in the end the merge buffer),
   // then 16 bytes a sequence
-  static constexpr int SMEM = MAIN;
-  static constexpr int SLOT = ROWS * (HD + 2);      // floats of a partial result
+  static constexpr int SMEM = W * WARP_BYTES > MERGE ? W * WARP_BYTES : MERGE;
+  // a partial result: accumulators, m and l, m and l of the group merged here
+  static constexpr int SLOT = ROWS * (HD + 4);
   // what a segment costs besides its blocks, in blocks: its rows of Q, the
   // first copy's latency and its end
-  static constexpr int OVERHEAD = 4;
+  static constexpr int OVERHEAD = 6;
+  // the least a run has, so that short contexts are not cut into pieces
+  // whose merge costs more than they do
+  static constexpr int LEAST = OVERHEAD + 4;
 };
 
 __device__ __forceinline__ void kv_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -277,49 +276,94 @@ __device__ __forceinline__ void kv_store4(void* p, int type, int64_t at, float4 
         make_uint2(kv_pack2<kRowF16>(v.x, v.y), kv_pack2<kRowF16>(v.z, v.w));
 }
 
-// Stores 4 channels of a row of a segment: O / l, times D_v^{-1/2}.
+// Stores 4 channels of a row: O / l, times D_v^{-1/2}; at: the row's first
+// element in Y.
 template <int HD>
-__device__ __forceinline__ void kv_store_row(const KvAttentionArgs& a, int row0, int h, int r, int ch, float4 o,
-                                             float l) {
-  const float f = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // l = 0: nothing seen; NaN stays
+__device__ __forceinline__ void kv_store_row(const KvAttentionArgs& a, int64_t at, int h, int ch, float4 o, float l) {
+  const float f = l > 0.f ? 1.f / l : l;            // l = 0: nothing seen, O = 0; NaN stays
   o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-  if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.Dv != nullptr) {
     const float4 d = __ldg(reinterpret_cast<const float4*>(a.Dv + h * HD + ch));
     o = make_float4(o.x * d.x, o.y * d.y, o.z * d.z, o.w * d.w);
   }
-  const int64_t row = row0 + r / a.per;
-  const int head = h * a.per + r % a.per;
-  kv_store4(a.Y, a.y_type, (row * a.heads + head) * HD + ch, o);
+  kv_store4(a.Y, a.y_type, at + ch, o);
 }
+
+// How the units of work are cut into runs: run i is [start(i), start(i + 1)).
+struct KvRuns {
+  int64_t total, each;
+  int runs, more;                                   // the first `more` runs have one unit more
+  __device__ __forceinline__ int64_t start(int i) const { return i * each + min(i, more); }
+  __device__ __forceinline__ int of(int64_t unit) const {
+    const int64_t cut = more * (each + 1);
+    return static_cast<int>(unit < cut ? unit / (each + 1) : more + (unit - cut) / each);
+  }
+};
+
+// The partial results of a segment that several runs share: runs `first` to
+// `last` have one each, but a thread block in [block0, block1), all of whose
+// runs are the segment's, has one in all, in its first run's place.
+struct KvParts {
+  int first, last, block0, block1, W, n;
+  __device__ __forceinline__ KvParts(const KvRuns& r, int64_t begin, int64_t end, int overhead, int warps) : W(warps) {
+    first = r.of(begin + overhead);
+    last = r.of(end - 1);
+    int lo = r.of(begin);
+    if (r.start(lo) != begin) ++lo;                 // the first run wholly in the segment
+    const int hi = r.start(last + 1) == end ? last + 1 : last;
+    block0 = (lo + W - 1) / W;
+    block1 = hi / W;
+    if (block1 <= block0) {
+      block0 = block1 = 0;
+      n = last - first + 1;
+    } else {
+      n = block1 - block0 + max(block0 * W - first, 0) + last + 1 - block1 * W;
+    }
+  }
+  // the run that holds result k (0 <= k < n), and the result that run r holds
+  __device__ __forceinline__ int run(int k) const {
+    if (block1 == 0) return first + k;
+    const int before = max(block0 * W - first, 0);
+    if (k < before) return first + k;
+    k -= before;
+    return k < block1 - block0 ? (block0 + k) * W : block1 * W + k - (block1 - block0);
+  }
+  __device__ __forceinline__ int index(int r) const {
+    if (block1 == 0 || r < block0 * W) return r - first;
+    const int before = max(block0 * W - first, 0);
+    return r < block1 * W ? before + r / W - block0 : before + block1 - block0 + r - block1 * W;
+  }
+  __device__ __forceinline__ bool merged(int r) const { return r >= block0 * W && r < block1 * W; }
+};
 
 template <int HD, int BITS, int NG, int NT>
 __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAttention<HD, BITS, NG, NT>::CTAS)
     kv_attention_kernel(const KvAttentionArgs a) {
   using A = KvAttention<HD, BITS, NG, NT>;
   using F = typename A::F;
-  constexpr int W = A::W, ROWS = A::ROWS, KS = A::KS, MT = A::MT, STAGES = A::STAGES, BP = A::BP;
-  constexpr int WORDS = F::LB / 4;              // words of a lane's half
-  constexpr int PW = F::PIECE / 4;              // of a piece
+  constexpr int W = A::W, ROWS = A::ROWS, KS = A::KS, MT = A::MT, STAGES = A::STAGES, OV = A::OVERHEAD;
+  constexpr int PW = F::PIECE / 4;              // words of a lane's piece
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t all_bars[W * STAGES];
-  __shared__ int all_absent[W * STAGES];        // bit u: the stage's block u has no page or is none
+  __shared__ int all_absent[W * STAGES];        // the stage's block has no page
   __shared__ float warp_m[W][ROWS], warp_l[W][ROWS];
-  __shared__ int abort_flag;
+  __shared__ KvRuns runs_s;
+  __shared__ int abort_flag, last_flag;
   const KvGeometry& g = a.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, tq = lane & 3;      // row group and quarter of the MMA fragments
   uint8_t* ring = smem + warp * A::WARP_BYTES;
-  uint32_t* qfrag = reinterpret_cast<uint32_t*>(ring + STAGES * A::STAGE);
-  uint64_t* row_mask = reinterpret_cast<uint64_t*>(ring + STAGES * A::STAGE + A::QFRAG);
-  float* q_factor = reinterpret_cast<float*>(row_mask + ROWS);   // t = <row, (c - z) s> * q_factor
+  uint32_t* qfrag = reinterpret_cast<uint32_t*>(ring + STAGES * F::BLOCK);
+  uint64_t* row_mask = reinterpret_cast<uint64_t*>(ring + STAGES * F::BLOCK + A::QFRAG);
+  int64_t* row_y = reinterpret_cast<int64_t*>(row_mask + ROWS);  // the row's first element in Y; -1: not there
+  float* q_factor = reinterpret_cast<float*>(row_y + ROWS);      // t = <row, (c - z) s> * q_factor
   int* row_pos = reinterpret_cast<int*>(q_factor + ROWS);
   float* q_sum = reinterpret_cast<float*>(row_pos + ROWS);       // [NG][ROWS] sums of a row's group
   float* q_off = q_sum + NG * ROWS;                              // the same with the fields' offsets as weights
   uint64_t* bars = all_bars + warp * STAGES;
   int* absent = all_absent + warp * STAGES;
   // {end of its work in blocks of one head (56 bits), n (8 bits); kv; row0}
-  int4* seqs = reinterpret_cast<int4*>(smem + A::MAIN);
+  int4* seqs = reinterpret_cast<int4*>(smem + A::SMEM);
   auto pack = [](int64_t end, int n, int kv, int row0) {
     return make_int4(static_cast<int>(end), static_cast<int>((end >> 32) & 0xFFFFFF) | n << 24, kv, row0);
   };
@@ -335,58 +379,55 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
   if (tid == 0) abort_flag = 0;
   grid_dependency_wait();
 
-  // ---- the work of every sequence and its running sum
+  // ---- the work of every sequence, its running sum, and the runs
   auto first_block = [&](int kv, int n) -> int {   // of those a new token may see
     if (a.window <= 0) return 0;
     const int64_t p = static_cast<int64_t>(kv) - n - a.window + 1;
     return p > 0 ? static_cast<int>(p >> 4) : 0;
   };
   auto tiles_of = [&](int n) { return (n * a.per + ROWS - 1) / ROWS; };
-  for (int b = tid; b < g.batch; b += W * 32) {
-    KvSequence s;
-    int64_t w = 0;
-    if (kv_sequence(g, b, s)) {
-      if (s.n > 0) w = static_cast<int64_t>(((s.kv - 1) >> 4) + 1 - first_block(s.kv, s.n) + A::OVERHEAD) * tiles_of(s.n);
-    } else {
-      if (blockIdx.x == 0 && s.n != 0) set_flag(g.status, TTQ_FLAG_BAD_INDEX);
-      s.n = 0;
-    }
-    seqs[b] = pack(w, s.n, s.kv, s.row0);
-  }
-  __syncthreads();
   if (warp == 0) {
     int64_t base = 0;
     for (int b0 = 0; b0 < g.batch; b0 += 32) {
       const int b = b0 + lane;
-      const int4 q = b < g.batch ? seqs[b] : make_int4(0, 0, 0, 0);
-      int64_t v = end_of(q);
+      KvSequence s = {};
+      int64_t v = 0;
+      if (b < g.batch) {
+        if (kv_sequence(g, b, s)) {
+          if (s.n > 0) v = static_cast<int64_t>(((s.kv - 1) >> 4) + 1 - first_block(s.kv, s.n) + OV) * tiles_of(s.n);
+        } else {
+          if (blockIdx.x == 0 && s.n != 0) set_flag(g.status, TTQ_FLAG_BAD_INDEX);
+          s.n = 0;
+        }
+      }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
       }
-      if (b < g.batch) seqs[b] = pack(base + v, q.y >> 24, q.z, q.w);
+      if (b < g.batch) seqs[b] = pack(base + v, s.n, s.kv, s.row0);
       base += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) {
+      const int64_t total = base * g.kv_heads, most = (total + A::LEAST - 1) / A::LEAST;
+      const int all = static_cast<int>(gridDim.x) * W, runs = most < all ? static_cast<int>(most) : all;
+      runs_s.total = total;
+      runs_s.runs = runs;
+      runs_s.each = runs > 0 ? total / runs : 0;
+      runs_s.more = static_cast<int>(total - runs_s.each * runs);
     }
   }
   __syncthreads();
-  const int64_t total = g.batch > 0 ? end_of(seqs[g.batch - 1]) * g.kv_heads : 0;
-  // no run shorter than a segment's overhead and a few blocks, so that short
-  // contexts are not cut into pieces whose merge costs more than they do
-  constexpr int LEAST = A::OVERHEAD + 4;
-  const int64_t most = (total + LEAST - 1) / LEAST, all = static_cast<int64_t>(gridDim.x) * W;
-  const int64_t runs = most < all ? most : all;
-  const int64_t run = static_cast<int64_t>(blockIdx.x) * W + warp;
-  int4* meta = a.meta + 2 * run;
-  if (lane == 0) meta[0] = make_int4(-1, 0, 0, 0);
-  // a block's warps all have work or, but for the last, none
-  int64_t x = run < runs ? run * total / runs : 0;
-  const int64_t x1 = run < runs ? (run + 1) * total / runs : 0;
+  const KvRuns runs = runs_s;
+  if (static_cast<int>(blockIdx.x) * W >= runs.runs) return;
+  const int run = static_cast<int>(blockIdx.x) * W + warp;
+  int64_t x = run < runs.runs ? runs.start(run) : 0;
+  const int64_t x1 = run < runs.runs ? runs.start(run + 1) : 0;
 
-  // ---- the segment at x; a segment's blocks follow A::OVERHEAD units of its
-  // own cost, so a run that begins within those begins with its first block
+  // ---- the segment at x; a segment's blocks follow OV units of its own
+  // cost, so a run that begins within those begins with its first block
   KvSegment seg = {};
-  int from = 0, count = 0, tiles = 1;
+  int tiles = 1;
   int64_t left = 0;                             // units of the segment from x on
   auto enter = [&](int b) {                     // sequence b's first segment
     while (((seqs[b].y >> 24) & 0xFF) == 0) ++b;   // there is one: x < total
@@ -405,27 +446,19 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     }
     enter(lo);
     const int64_t rest = x - (lo > 0 ? end_of(seqs[lo - 1]) * g.kv_heads : 0);
-    const int64_t units = seg.blocks + A::OVERHEAD, tile = rest / units;
+    const int64_t units = seg.blocks + OV, tile = rest / units;
     left = units - (rest - tile * units);
-    seg.h = static_cast<int>(tile / tiles);
-    seg.tile = static_cast<int>(tile - static_cast<int64_t>(seg.h) * tiles);
+    seg.h = static_cast<int>(tile) / tiles;
+    seg.tile = static_cast<int>(tile) - seg.h * tiles;
   }
-  // whether the whole thread block works on one segment, this run's first:
-  // then its partial results are merged in shared memory
-  const int64_t block_end = (static_cast<int64_t>(blockIdx.x) * W + W) * total / (runs > 0 ? runs : 1);
-  bool together = run < runs && (blockIdx.x + 1) * W <= runs && block_end <= x + left;
-  {
-    const int64_t key = together ? (static_cast<int64_t>(seg.b) << 40 | static_cast<int64_t>(seg.h) << 24 | seg.tile) : -1;
-    __shared__ int64_t keys[W];
-    if (lane == 0) keys[warp] = key;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < W; ++w) together = together && keys[w] == keys[0] && keys[w] >= 0;
-  }
-  if (tid == 0) a.together[blockIdx.x] = together;
+  // whether all runs of this thread block are one segment's: the block's
+  // units lie within the segment of this run (then of all its runs)
+  const bool together = (static_cast<int>(blockIdx.x) + 1) * W <= runs.runs &&
+                        runs.start(static_cast<int>(blockIdx.x) * W) >= x + left - seg.blocks - OV &&
+                        runs.start((static_cast<int>(blockIdx.x) + 1) * W) <= x + left;
 
   const KvMagic<BITS> magic;
-  uint32_t phases = 0;                          // bit s: parity of stage s
+  int turn = 0;                                 // blocks waited for so far: stage and parity of the ring
   bool ok = true;
   for (bool started = false; x < x1 && ok; started = true) {
     if (started && left == 0) {                 // the next segment
@@ -433,76 +466,70 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         seg.tile = 0;
         if (++seg.h == g.kv_heads) enter(seg.b + 1);
       }
-      left = seg.blocks + A::OVERHEAD;
+      left = seg.blocks + OV;
     }
     // blocks [from, from + count) of it are this run's; none if only a part
     // of its overhead is
     const int64_t take = x1 - x < left ? x1 - x : left;
-    from = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks);
+    const int from = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks);
     x += take;
     left -= take;
-    count = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks) - from;
-    const bool whole = count == seg.blocks;
+    const int count = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks) - from;
     const int old = seg.kv - seg.n;             // positions before the new ones
     const int R = seg.n * a.per, r0 = seg.tile * ROWS;
-    // (a run of overhead alone goes on below with no blocks: nothing is
-    // stored unless the block merges its warps' results)
+    // (a run of overhead alone leaves no result of its own; within a block
+    // whose warps merge theirs it goes on without blocks)
     if (count == 0 && !together) continue;
 
-    // ---- start the copies, BP blocks a stage
+    // ---- start the copies
     const int blk0 = seg.first + from;          // this run's first block of the segment
-    const int steps = (count + BP - 1) / BP;
     const uint8_t* src = nullptr;               // this lane's block 32 k + lane
-    const uint8_t* src_next = nullptr;
-    auto load_sources = [&](int i0) {
-      const int i = i0 + lane, blk = blk0 + i;
-      src = nullptr;
-      if (i < count) {
-        const int pg = blk / g.page_blocks, page = g.table[seg.b * g.table_stride + pg];
-        if (page >= 0 && page < g.num_pages)
-          src = g.pages + page * g.page_bytes +
-                (static_cast<int64_t>(seg.h) * g.page_blocks + (blk - pg * g.page_blocks)) * F::BLOCK;
-        else
-          set_flag(g.status, TTQ_FLAG_BAD_INDEX);
+    bool any_absent = false;
+    const int turn0 = turn;
+    auto issue = [&](int i) {                   // by the whole warp; one lane does it
+      if ((i & 31) == 0) {
+        const int j = i + lane, blk = blk0 + j;
+        src = nullptr;
+        if (j < count) {
+          const int pg = blk / g.page_blocks, page = g.table[seg.b * g.table_stride + pg];
+          if (page >= 0 && page < g.num_pages)
+            src = g.pages + page * g.page_bytes +
+                  (static_cast<int64_t>(seg.h) * g.page_blocks + (blk - pg * g.page_blocks)) * F::BLOCK;
+          else
+            set_flag(g.status, TTQ_FLAG_BAD_INDEX);
+        }
+        any_absent = __any_sync(0xffffffffu, j < count && src == nullptr) || any_absent;
       }
-      if constexpr (BP == 2)
-        src_next = reinterpret_cast<const uint8_t*>(
-            __shfl_down_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), 1));
-    };
-    auto issue = [&](int step) {                // by the whole warp; one lane does it
-      const int i = step * BP, s = step % STAGES;
-      if ((i & 31) == 0) load_sources(i);
       if (lane == (i & 31)) {
-        const uint32_t dst = smem_addr(ring + s * A::STAGE);
-        if constexpr (BP == 1) {
-          absent[s] = src == nullptr;
-          if (src != nullptr) {
-            mbar_arrive_expect_tx(&bars[s], F::BLOCK);
-            bulk_load(dst, src, F::BLOCK, &bars[s]);
-          } else {
-            mbar_arrive(&bars[s]);
-          }
+        const int s = (turn0 + i) % STAGES;
+        absent[s] = src == nullptr;
+        if (src != nullptr) {
+          mbar_arrive_expect_tx(&bars[s], F::BLOCK);
+          bulk_load(smem_addr(ring + s * F::BLOCK), src, F::BLOCK, &bars[s]);
         } else {
-          absent[s] = (src == nullptr) | (src_next == nullptr) << 1;
-          if (src != nullptr && src_next == src + F::BLOCK) {
-            mbar_arrive_expect_tx(&bars[s], 2 * F::BLOCK);
-            bulk_load(dst, src, 2 * F::BLOCK, &bars[s]);
-          } else {
-            const uint32_t bytes = (src != nullptr ? F::BLOCK : 0) + (src_next != nullptr ? F::BLOCK : 0);
-            if (bytes != 0) mbar_arrive_expect_tx(&bars[s], bytes);
-            else mbar_arrive(&bars[s]);
-            if (src != nullptr) bulk_load(dst, src, F::BLOCK, &bars[s]);
-            if (src_next != nullptr) bulk_load(dst + F::BLOCK, src_next, F::BLOCK, &bars[s]);
-          }
+          mbar_arrive(&bars[s]);
         }
       }
     };
     int issued = 0;
-    for (; issued < STAGES && issued < steps; ++issued) issue(issued);
+    for (; issued < STAGES && issued < count; ++issued) issue(issued);
 
     // ---- the tile's rows of Q as B fragments, and what each row sees
-    if (count > 0) {
+    {
       constexpr int E = HD / 32;                // consecutive channels of a lane
+      int64_t q_at = -1;                        // row `lane` of the tile in Q
+      if (lane < ROWS) {
+        const int rr = r0 + lane, i_new = rr / a.per, head = seg.h * a.per + rr - i_new * a.per;
+        const int64_t row = seg.row0 + i_new;
+        uint64_t mask = 0;
+        if (rr < R) {
+          q_at = row * a.q_row + head * a.q_head;
+          mask = a.tree != nullptr ? a.tree[row] : (2ull << i_new) - 1ull;
+        }
+        row_y[lane] = rr < R ? (row * a.heads + head) * HD : -1;
+        row_mask[lane] = mask;
+        row_pos[lane] = old + __popcll(mask & ~(1ull << (i_new & 63)));
+      }
       float dk[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) dk[e] = a.Dk != nullptr ? __ldg(a.Dk + seg.h * HD + lane * E + e) : 1.f;
@@ -511,14 +538,10 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         float v[8][E];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int rr = r0 + nt * 8 + k;
+          const int64_t at = __shfl_sync(0xffffffffu, q_at, nt * 8 + k);
 #pragma unroll
           for (int e = 0; e < E; ++e) v[k][e] = 0.f;
-          if (rr < R) {
-            const int i_new = rr / a.per;
-            kv_load_lane<E>(a.Q, a.q_type,
-                            (seg.row0 + i_new) * a.q_row + (seg.h * a.per + rr - i_new * a.per) * a.q_head + lane * E, v[k]);
-          }
+          if (at >= 0) kv_load_lane<E>(a.Q, a.q_type, at + lane * E, v[k]);
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -544,17 +567,10 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           if (lane == 0) q_factor[r] = a.scale * up * (a.cap > 0.f ? 1.f / a.cap : kKvLog2e);
         }
       }
-      if (lane < ROWS) {
-        const int rr = r0 + lane, i_new = rr / a.per;
-        uint64_t mask = 0;
-        if (rr < R) mask = a.tree != nullptr ? a.tree[seg.row0 + i_new] : (2ull << i_new) - 1ull;
-        row_mask[lane] = mask;
-        row_pos[lane] = old + __popcll(mask & ~(1ull << (i_new & 63)));
-      }
       __syncwarp();
       if constexpr (BITS != 8) {
         // the sums of each group of the rounded rows: the first product with
-        // ones, and with the offsets, as codes
+        // ones, and (INT2, whose fields' offsets differ) with the offsets, as codes
 #pragma unroll
         for (int k = 0; k < NG; ++k)
 #pragma unroll
@@ -564,11 +580,12 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
             for (int j = 0; j < KS / NG; ++j) {
               const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * KS + k * (KS / NG) + j) * 32 + lane) * 2);
               kv_mma(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, bq.x, bq.y);
-              kv_mma(off, A::EVEN, A::EVEN, A::ODD, A::ODD, bq.x, bq.y);
+              if constexpr (BITS == 2) kv_mma(off, A::EVEN, A::EVEN, A::ODD, A::ODD, bq.x, bq.y);
             }
             if (gr == 0) {
               *reinterpret_cast<float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq) = make_float2(one[0], one[1]);
-              *reinterpret_cast<float2*>(q_off + k * ROWS + 8 * nt + 2 * tq) = make_float2(off[0], off[1]);
+              if constexpr (BITS == 2)
+                *reinterpret_cast<float2*>(q_off + k * ROWS + 8 * nt + 2 * tq) = make_float2(off[0], off[1]);
             }
           }
         __syncwarp();
@@ -577,10 +594,11 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 
     // ---- the loop over this run's blocks
     float o[MT][NT][4] = {};
-    float m[NT][2], l[NT][2] = {};
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = kKvFloor;
-    int e_run = 0;                              // running exponent field of V's scales (binary32's; 0: none yet)
+    float m[NT][2] = {}, l[NT][2] = {};
+    constexpr uint32_t ALL = (1u << (2 * NT)) - 1;
+    uint32_t seen = 0;                          // columns (bit 2 nt + c) whose maximum is a score's
+    bool all_seen = false;                      // all columns of all lanes
+    float vf = 1.2676506e30f;                   // 2^-E; at first 2^100, so that any scale lowers it
     float zs[A::VRAW ? NG : 1][4] = {};         // sums of p s (offset + z) 2^-E per group
     // takes the offsets and zeros off the accumulators, often enough that the
     // sums of offset codes do not grow much past their difference
@@ -594,307 +612,282 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         for (int k = 0; k < NG; ++k) zs[k][0] = zs[k][1] = zs[k][2] = zs[k][3] = 0.f;
       }
     };
-    // steps [0, plain0) and [plain1, steps) need masks: blocks that the window
-    // of the last new token does not cover, those that reach the new tokens,
-    // and a last step that is not full
-    int plain0 = 0, plain1;
-    {
-      const int64_t past = static_cast<int64_t>(seg.kv) - a.window;   // p >= past is in every row's window
-      if (a.window > 0 && past > 0) {
-        const int64_t need = (past + 15) / 16 - blk0;                 // first block wholly in it
-        plain0 = need <= 0 ? 0 : need >= count ? steps : static_cast<int>((need + BP - 1) / BP);
+    auto rescale = [&](int nt, int c, float f) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        o[mt][nt][c] *= f;
+        o[mt][nt][c + 2] *= f;
       }
-      const int full = (old >> 4) - blk0;                             // blocks before the new tokens
-      plain1 = (full < 0 ? 0 : full < count ? full : count) / BP;
+      if constexpr (A::VRAW) {
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+          zs[k][c] *= f;
+          zs[k][c + 2] *= f;
+        }
+      }
+    };
+    // blocks [plain0, plain1) need no masks: not those that the window of the
+    // last new token does not cover, nor those that reach the new tokens
+    int plain0 = 0;
+    if (a.window > 0 && seg.kv > a.window) {
+      const int64_t past = static_cast<int64_t>(seg.kv) - a.window;   // p >= past is in every row's window
+      const int64_t need = (past + 15) / 16 - blk0;                   // first block wholly in it
+      plain0 = need <= 0 ? 0 : need >= count ? count : static_cast<int>(need);
     }
+    const int plain1 = (old >> 4) - blk0;                             // blocks before the new tokens
 
-    auto process = [&](auto masked_c, uint32_t st, int blk, int gone) {
+    auto process = [&](auto masked_c, uint32_t st, int blk, bool gone) {
       constexpr bool MASKED = decltype(masked_c)::value;
       // -- scores
-      float s[BP][NT][4];
-      uint32_t kp[BP][2][NG];
-#pragma unroll
-      for (int u = 0; u < BP; ++u) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
-        kv_lds<NG>(st + u * F::BLOCK + F::CODES + gr * NG * 4, kp[u][0]);
-        kv_lds<NG>(st + u * F::BLOCK + F::CODES + (gr + 8) * NG * 4, kp[u][1]);
-      }
+      float s[NT][4];
+      uint32_t kp[2][NG];
+      kv_lds<NG>(st + F::CODES + gr * NG * 4, kp[0]);
+      kv_lds<NG>(st + F::CODES + (gr + 8) * NG * 4, kp[1]);
       constexpr int KSG = KS / NG;              // k steps of a group
       constexpr int KSW = BITS == 8 ? 1 : 32 / BITS / 4;   // k steps of a word
-      uint32_t kw[BP][2][PW], pa[BP][2][2 * KSW];
+      uint32_t kw[2][PW], pa[2][2 * KSW];
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
-        float acc[BP][NT][4];
+        float acc[NT][4];
 #pragma unroll
-        for (int u = 0; u < BP; ++u)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) acc[u][nt][0] = acc[u][nt][1] = acc[u][nt][2] = acc[u][nt][3] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 #pragma unroll
         for (int j = 0; j < KSG; ++j) {
           const int ks = k * KSG + j, w = ks / KSW, in = ks % KSW;
 #pragma unroll
-          for (int u = 0; u < BP; ++u)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              if (in == 0 && w % PW == 0)
-                kv_lds<PW>(st + u * F::BLOCK + (w / PW * 2 + r) * 32 * F::PIECE + lane * F::PIECE, kw[u][r]);
-              if (in == 0) {
-                if constexpr (BITS == 8) kv_e4m3x4(kw[u][r][w % PW], pa[u][r][0], pa[u][r][1]);
-                else kv_offset_pairs<BITS>(kw[u][r][w % PW], magic, pa[u][r]);
-              }
+          for (int r = 0; r < 2; ++r) {
+            if (in == 0 && w % PW == 0)
+              kv_lds<PW>(st + (w / PW * 2 + r) * 32 * F::PIECE + lane * F::PIECE, kw[r]);
+            if (in == 0) {
+              if constexpr (BITS == 8) kv_e4m3x4(kw[r][w % PW], pa[r][0], pa[r][1]);
+              else kv_offset_pairs<BITS>(kw[r][w % PW], magic, pa[r]);
             }
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * KS + ks) * 32 + lane) * 2);
-#pragma unroll
-            for (int u = 0; u < BP; ++u)
-              kv_mma(acc[u][nt], pa[u][0][2 * in], pa[u][1][2 * in], pa[u][0][2 * in + 1], pa[u][1][2 * in + 1], bq.x, bq.y);
+            kv_mma(acc[nt], pa[0][2 * in], pa[1][2 * in], pa[0][2 * in + 1], pa[1][2 * in + 1], bq.x, bq.y);
           }
         }
+        const float2 p0 = __half22float2(u32_as_h2(kp[0][k])), p1 = __half22float2(u32_as_h2(kp[1][k]));
 #pragma unroll
-        for (int u = 0; u < BP; ++u) {
-          const float2 p0 = __half22float2(u32_as_h2(kp[u][0][k])), p1 = __half22float2(u32_as_h2(kp[u][1][k]));
-          const float s0 = p0.x, s1 = p1.x;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (BITS != 8) {
-              const float2 qs = *reinterpret_cast<const float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq);
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (BITS != 8) {
+            const float2 qs = *reinterpret_cast<const float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq);
+            float z0 = p0.y, z1 = p1.y;
+            if constexpr (BITS == 4) {          // both fields are offset by 64
+              z0 += 64.f, z1 += 64.f;
+            } else {
               const float2 qo = *reinterpret_cast<const float2*>(q_off + k * ROWS + 8 * nt + 2 * tq);
-              acc[u][nt][0] = fmaf(-p0.y, qs.x, acc[u][nt][0] - qo.x);
-              acc[u][nt][1] = fmaf(-p0.y, qs.y, acc[u][nt][1] - qo.y);
-              acc[u][nt][2] = fmaf(-p1.y, qs.x, acc[u][nt][2] - qo.x);
-              acc[u][nt][3] = fmaf(-p1.y, qs.y, acc[u][nt][3] - qo.y);
+              acc[nt][0] -= qo.x, acc[nt][1] -= qo.y, acc[nt][2] -= qo.x, acc[nt][3] -= qo.y;
             }
-            s[u][nt][0] = fmaf(acc[u][nt][0], s0, s[u][nt][0]);
-            s[u][nt][1] = fmaf(acc[u][nt][1], s0, s[u][nt][1]);
-            s[u][nt][2] = fmaf(acc[u][nt][2], s1, s[u][nt][2]);
-            s[u][nt][3] = fmaf(acc[u][nt][3], s1, s[u][nt][3]);
+            acc[nt][0] = fmaf(-z0, qs.x, acc[nt][0]);
+            acc[nt][1] = fmaf(-z0, qs.y, acc[nt][1]);
+            acc[nt][2] = fmaf(-z1, qs.x, acc[nt][2]);
+            acc[nt][3] = fmaf(-z1, qs.y, acc[nt][3]);
+          }
+          if (k == 0) {
+            s[nt][0] = acc[nt][0] * p0.x, s[nt][1] = acc[nt][1] * p0.x;
+            s[nt][2] = acc[nt][2] * p1.x, s[nt][3] = acc[nt][3] * p1.x;
+          } else {
+            s[nt][0] = fmaf(acc[nt][0], p0.x, s[nt][0]);
+            s[nt][1] = fmaf(acc[nt][1], p0.x, s[nt][1]);
+            s[nt][2] = fmaf(acc[nt][2], p1.x, s[nt][2]);
+            s[nt][3] = fmaf(acc[nt][3], p1.x, s[nt][3]);
           }
         }
       }
-      // -- V's scales of tokens gr and gr + 8, and the exponent of the largest
-      // over all of V (NaN aside); tokens that are not there count for nothing
-      int there[BP];                            // tokens of the block
-      float vs[BP][2][NG];
-      {
-        float top = 0.f;
+      // -- V's scales of tokens gr and gr + 8; tokens that are not there count
+      // for nothing
+      const int there = MASKED ? (gone ? 0 : seg.kv - blk * 16) : 16;   // tokens of the block
+      float vs[2][NG];
+      bool higher = !all_seen;                  // a scale or a score is well above the running ones
 #pragma unroll
-        for (int u = 0; u < BP; ++u) {
-          there[u] = MASKED ? ((gone >> u & 1) ? 0 : seg.kv - (blk + u) * 16) : 16;
+      for (int r = 0; r < 2; ++r) {
+        uint32_t vp[NG];
+        kv_lds<NG>(st + F::V_OFFSET + F::CODES + (gr + 8 * r) * NG * 4, vp);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            uint32_t vp[NG];
-            kv_lds<NG>(st + u * F::BLOCK + F::V_OFFSET + F::CODES + (gr + 8 * r) * NG * 4, vp);
-#pragma unroll
-            for (int k = 0; k < NG; ++k) {
-              vs[u][r][k] = __half2float(u32_as_h2(vp[k]).x);
-              if (MASKED && gr + 8 * r >= there[u]) vs[u][r][k] = 0.f;
-              top = fmaxf(top, vs[u][r][k]);
-            }
-          }
-        }
-        const int e_new = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23);
-        if (e_new > e_run) {
-          const float f = e_run == 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + e_run - e_new) << 23);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f;
-          if constexpr (A::VRAW) {
-#pragma unroll
-            for (int k = 0; k < NG; ++k)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) zs[k][i] *= f;
-          }
-          e_run = e_new;
+        for (int k = 0; k < NG; ++k) {
+          vs[r][k] = __half2float(u32_as_h2(vp[k]).x);
+          if (MASKED && gr + 8 * r >= there) vs[r][k] = 0.f;
+          higher |= vs[r][k] * vf > 64.f;
         }
       }
-      // -- scores in powers of two, masks
-      bool higher = false;
+      // -- scores in powers of two less the running maximum, masks
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float2 f = *reinterpret_cast<const float2*>(q_factor + 8 * nt + 2 * tq);
-#pragma unroll
-        for (int u = 0; u < BP; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[u][nt][i] *= (i & 1) ? f.y : f.x;
-      }
-      if (a.cap > 0.f) {      // cap tanh(t) = cap (1 - 2 / (1 + e^{2 t}))
-#pragma unroll
-        for (int u = 0; u < BP; ++u)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              s[u][nt][i] = a.cap * kKvLog2e * (1.f - 2.f * kv_rcp(1.f + kv_exp2(s[u][nt][i] * (2.f * kKvLog2e))));
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int u = 0; u < BP; ++u)
+        if (a.cap > 0.f) {    // cap tanh(t) = cap (1 - 2 / (1 + e^{2 t}))
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if constexpr (MASKED) {
-              const int j = (i & 2) ? gr + 8 : gr, p = (blk + u) * 16 + j, row = 8 * nt + 2 * tq + (i & 1);
-              bool see = j < there[u];
-              if (see && p >= old) {
-                see = (row_mask[row] >> (p - old)) & 1ull;
-                if (see && a.window > 0) {
-                  const int k_new = p - old;
-                  const uint64_t mask = a.tree != nullptr ? a.tree[seg.row0 + k_new] : (2ull << k_new) - 1ull;
-                  see = row_pos[row] - old - __popcll(mask & ~(1ull << k_new)) < a.window;
-                }
-              } else if (see && a.window > 0) {
-                see = row_pos[row] - p < a.window;
-              }
-              if (!see) s[u][nt][i] = -INFINITY;
-            }
-            higher |= s[u][nt][i] > m[nt][i & 1] + kKvSlack;
+            const float t = s[nt][i] * ((i & 1) ? f.y : f.x);
+            s[nt][i] = a.cap * kKvLog2e * (1.f - 2.f * kv_rcp(1.f + kv_exp2(t * (2.f * kKvLog2e)))) - m[nt][i & 1];
           }
-      // -- the running maximum moves only when a score is well above it
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][i] = fmaf(s[nt][i], (i & 1) ? f.y : f.x, -m[nt][i & 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (MASKED) {
+            const int j = (i & 2) ? gr + 8 : gr, p = blk * 16 + j, row = 8 * nt + 2 * tq + (i & 1);
+            bool see = j < there;
+            if (see && p >= old) {
+              see = (row_mask[row] >> (p - old)) & 1ull;
+              if (see && a.window > 0) {
+                const int k_new = p - old;
+                const uint64_t mask = a.tree != nullptr ? a.tree[seg.row0 + k_new] : (2ull << k_new) - 1ull;
+                see = row_pos[row] - old - __popcll(mask & ~(1ull << k_new)) < a.window;
+              }
+            } else if (see && a.window > 0) {
+              see = row_pos[row] - p < a.window;
+            }
+            if (!see) s[nt][i] = -INFINITY;
+          }
+          higher |= s[nt][i] > kKvSlack;
+        }
+      }
+      // -- the running maxima move only then (and to a column's first score)
       if (__any_sync(0xffffffffu, higher)) {
+        float top = 0.f;                        // the largest scale (NaN aside)
+#pragma unroll
+        for (int k = 0; k < NG; ++k) top = fmaxf(top, fmaxf(vs[0][k], vs[1][k]));
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+        float fv = 1.f;
+        if (top * vf > 64.f) {
+          // 2^-e for a scale in [2^e, 2^(e + 1)): its exponent's complement
+          const float vf_new = __uint_as_float((254u - (__float_as_uint(top) >> 23)) << 23);
+          fv = vf_new / vf;
+          vf = vf_new;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = m[nt][c];
-#pragma unroll
-            for (int u = 0; u < BP; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][c], s[u][nt][c + 2]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float f = kv_exp2(m[nt][c] - mx);
-            m[nt][c] = mx;
+            float up = fmaxf(s[nt][c], s[nt][c + 2]);
+            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
+            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
+            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
+            const uint32_t bit = 1u << (2 * nt + c);
+            // (each column by its own scores, so that no row's result depends on another's)
+            if (!(up > -INFINITY) || ((seen & bit) && up <= kKvSlack)) up = 0.f;
+            else seen |= bit;
+            // (before the first score l and o are zero, or NaN)
+            const float f = up < 0.f ? 1.f : kv_exp2(-up);
+            m[nt][c] += up;
+            s[nt][c] -= up;
+            s[nt][c + 2] -= up;
             l[nt][c] *= f;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              o[mt][nt][c] *= f;
-              o[mt][nt][c + 2] *= f;
-            }
-            if constexpr (A::VRAW) {
-#pragma unroll
-              for (int k = 0; k < NG; ++k) {
-                zs[k][c] *= f;
-                zs[k][c + 2] *= f;
-              }
-            }
+            rescale(nt, c, f * fv);
           }
+        all_seen = __all_sync(0xffffffffu, seen == ALL);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int u = 0; u < BP; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[u][nt][i] = kv_exp2(s[u][nt][i] - m[nt][i & 1]);
-            l[nt][i & 1] += s[u][nt][i];
-          }
+        for (int i = 0; i < 4; ++i) {
+          s[nt][i] = kv_exp2(s[nt][i]);
+          l[nt][i & 1] += s[nt][i];
+        }
       // -- p s_V 2^-E as the B operand, and the second product
-      const float vf = __uint_as_float(static_cast<uint32_t>(253 - (e_run == 0 ? 126 : e_run)) << 23);   // s vf < 1
       constexpr int MTG = MT / NG;              // m tiles of a group
       constexpr int MTW = BITS == 8 ? 1 : 16 / BITS / 2;   // m tiles of a word
+      const uint32_t vst = st + F::V_OFFSET;
+      [[maybe_unused]] uint32_t vz[2][NG], keep[2] = {};   // zeros of tokens 2 tq, 2 tq + 1 (+ 8)
 #pragma unroll
-      for (int u = 0; u < BP; ++u) {
-        const uint32_t vst = st + u * F::BLOCK + F::V_OFFSET;
-        [[maybe_unused]] uint32_t vz[2][NG], keep[2] = {};   // zeros of tokens 2 tq, 2 tq + 1 (+ 8)
+      for (int r = 0; r < 2; ++r) {
+        if constexpr (MASKED) {
+          const int t0 = 2 * tq + 8 * r;
+          keep[r] = (t0 < there ? 0xFFFFu : 0u) | (t0 + 1 < there ? 0xFFFF0000u : 0u);
+        }
+        if constexpr (BITS != 8) {
+          uint32_t e[2 * NG];                   // both tokens' pairs are contiguous
+          kv_lds<NG == 1 ? 2 : 4>(vst + F::CODES + (2 * tq + 8 * r) * NG * 4, e);
+          if constexpr (NG == 4) kv_lds<4>(vst + F::CODES + (2 * tq + 8 * r) * NG * 4 + 16, e + 4);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if constexpr (MASKED) {
-            const int t0 = 2 * tq + 8 * r;
-            keep[r] = (t0 < there[u] ? 0xFFFFu : 0u) | (t0 + 1 < there[u] ? 0xFFFF0000u : 0u);
-          }
-          if constexpr (BITS != 8) {
-            uint32_t e0[NG], e1[NG];
-            kv_lds<NG>(vst + F::CODES + (2 * tq + 8 * r) * NG * 4, e0);
-            kv_lds<NG>(vst + F::CODES + (2 * tq + 1 + 8 * r) * NG * 4, e1);
-#pragma unroll
-            for (int k = 0; k < NG; ++k) {
-              vz[r][k] = __byte_perm(e0[k], e1[k], 0x7632);
-              if constexpr (MASKED) vz[r][k] &= keep[r];
-            }
+          for (int k = 0; k < NG; ++k) {
+            vz[r][k] = __byte_perm(e[k], e[NG + k], 0x7632);
+            if constexpr (MASKED) vz[r][k] &= keep[r];
           }
         }
-        uint32_t vw[2][PW], pv[2][BITS == 8 ? 2 : 16 / BITS];
+      }
+      uint32_t vw[2][PW], pv[2][BITS == 8 ? 2 : 16 / BITS];
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          const float s0 = vs[u][0][k] * vf, s1 = vs[u][1][k] * vf;
-          uint32_t b[NT][2];
+      for (int k = 0; k < NG; ++k) {
+        const float s0 = vs[0][k] * vf, s1 = vs[1][k] * vf;
+        uint32_t b[NT][2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float w0 = s[u][nt][0] * s0, w1 = s[u][nt][1] * s0, w2 = s[u][nt][2] * s1, w3 = s[u][nt][3] * s1;
-            if constexpr (MASKED) {             // a NaN scale reaches only those that see its token
-              w0 = s[u][nt][0] == 0.f ? 0.f : w0;
-              w1 = s[u][nt][1] == 0.f ? 0.f : w1;
-              w2 = s[u][nt][2] == 0.f ? 0.f : w2;
-              w3 = s[u][nt][3] == 0.f ? 0.f : w3;
-            }
-            b[nt][0] = kv_transpose(h2_as_u32(__floats2half2_rn(w0, w1)));
-            b[nt][1] = kv_transpose(h2_as_u32(__floats2half2_rn(w2, w3)));
+        for (int nt = 0; nt < NT; ++nt) {
+          float w0 = s[nt][0] * s0, w1 = s[nt][1] * s0, w2 = s[nt][2] * s1, w3 = s[nt][3] * s1;
+          if constexpr (MASKED) {               // a NaN scale reaches only those that see its token
+            w0 = s[nt][0] == 0.f ? 0.f : w0;
+            w1 = s[nt][1] == 0.f ? 0.f : w1;
+            w2 = s[nt][2] == 0.f ? 0.f : w2;
+            w3 = s[nt][3] == 0.f ? 0.f : w3;
           }
-          [[maybe_unused]] KvZero<BITS> z[2];
-          if constexpr (A::VRAW) {
-            // rows of even fields, then of odd ones
-            const uint32_t e0 = h2_as_u32(__hadd2(u32_as_h2(vz[0][k]), u32_as_h2(A::EVEN)));
-            const uint32_t e1 = h2_as_u32(__hadd2(u32_as_h2(vz[1][k]), u32_as_h2(A::EVEN)));
-            if constexpr (BITS == 4) {
-              kv_mma(zs[k], e0, e0, e1, e1, b[0][0], b[0][1]);
-            } else {
-              const uint32_t d0 = h2_as_u32(__hadd2(u32_as_h2(vz[0][k]), u32_as_h2(A::ODD)));
-              const uint32_t d1 = h2_as_u32(__hadd2(u32_as_h2(vz[1][k]), u32_as_h2(A::ODD)));
-              kv_mma(zs[k], e0, d0, e1, d1, b[0][0], b[0][1]);
-            }
-          } else if constexpr (BITS != 8) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) z[r].set(vz[r][k]);
+          b[nt][0] = kv_transpose(h2_as_u32(__floats2half2_rn(w0, w1)));
+          b[nt][1] = kv_transpose(h2_as_u32(__floats2half2_rn(w2, w3)));
+        }
+        [[maybe_unused]] KvZero<BITS> z[2];
+        if constexpr (A::VRAW) {
+          // rows of even fields, then of odd ones
+          const uint32_t e0 = h2_as_u32(__hadd2(u32_as_h2(vz[0][k]), u32_as_h2(A::EVEN)));
+          const uint32_t e1 = h2_as_u32(__hadd2(u32_as_h2(vz[1][k]), u32_as_h2(A::EVEN)));
+          if constexpr (BITS == 4) {
+            kv_mma(zs[k], e0, e0, e1, e1, b[0][0], b[0][1]);
+          } else {
+            const uint32_t d0 = h2_as_u32(__hadd2(u32_as_h2(vz[0][k]), u32_as_h2(A::ODD)));
+            const uint32_t d1 = h2_as_u32(__hadd2(u32_as_h2(vz[1][k]), u32_as_h2(A::ODD)));
+            kv_mma(zs[k], e0, d0, e1, d1, b[0][0], b[0][1]);
           }
+        } else if constexpr (BITS != 8) {
 #pragma unroll
-          for (int j = 0; j < MTG; ++j) {
-            const int mt = k * MTG + j, w = mt / MTW, in = mt % MTW;
+          for (int r = 0; r < 2; ++r) z[r].set(vz[r][k]);
+        }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              if (in == 0 && w % PW == 0) {
-                kv_lds<PW>(vst + (w / PW * 2 + r) * 32 * F::PIECE + lane * F::PIECE, vw[r]);
-                if constexpr (MASKED) {
+        for (int j = 0; j < MTG; ++j) {
+          const int mt = k * MTG + j, w = mt / MTW, in = mt % MTW;
 #pragma unroll
-                  for (int i = 0; i < PW; ++i) vw[r][i] &= keep[r];
-                }
-              }
-              if (in == 0 || (!A::VRAW && j == 0)) {
-                if constexpr (BITS == 8)        // bytes: even token's two channels, then the odd one's
-                  kv_e4m3x4(__byte_perm(vw[r][w % PW], 0, 0x3120), pv[r][0], pv[r][1]);
-                else if constexpr (A::VRAW)
-                  kv_offset_pairs<BITS>(vw[r][w % PW], magic, pv[r]);
-                else
-                  kv_int_pairs<BITS>(vw[r][w % PW], z[r], magic, pv[r]);
+          for (int r = 0; r < 2; ++r) {
+            if (in == 0 && w % PW == 0) {
+              kv_lds<PW>(vst + (w / PW * 2 + r) * 32 * F::PIECE + lane * F::PIECE, vw[r]);
+              if constexpr (MASKED) {
+#pragma unroll
+                for (int i = 0; i < PW; ++i) vw[r][i] &= keep[r];
               }
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              kv_mma(o[mt][nt], pv[0][2 * in], pv[0][2 * in + 1], pv[1][2 * in], pv[1][2 * in + 1], b[nt][0], b[nt][1]);
+            if (in == 0 || (!A::VRAW && j == 0)) {
+              if constexpr (BITS == 8)          // bytes: even token's two channels, then the odd one's
+                kv_e4m3x4(__byte_perm(vw[r][w % PW], 0, 0x3120), pv[r][0], pv[r][1]);
+              else if constexpr (A::VRAW)
+                kv_offset_pairs<BITS>(vw[r][w % PW], magic, pv[r]);
+              else
+                kv_int_pairs<BITS>(vw[r][w % PW], z[r], magic, pv[r]);
+            }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            kv_mma(o[mt][nt], pv[0][2 * in], pv[0][2 * in + 1], pv[1][2 * in], pv[1][2 * in + 1], b[nt][0], b[nt][1]);
         }
       }
     };
 
     int done = 0;
-    for (; done < steps; ++done) {
-      const int s = done % STAGES;
-      if (!mbar_wait(&bars[s], (phases >> s) & 1u, &abort_flag)) {
+    for (; done < count; ++done) {
+      const int s = (turn0 + done) % STAGES;
+      if (!mbar_wait(&bars[s], ((turn0 + done) / STAGES) & 1, &abort_flag)) {
         ok = false;
         break;
       }
-      phases ^= 1u << s;
-      const int gone = absent[s];
-      const uint32_t st = smem_addr(ring + s * A::STAGE);
-      if (gone != 0 || done < plain0 || done >= plain1) process(std::true_type{}, st, blk0 + done * BP, gone);
-      else process(std::false_type{}, st, blk0 + done * BP, 0);
+      const uint32_t st = smem_addr(ring + s * F::BLOCK);
+      const bool gone = any_absent && absent[s] != 0;
+      if (gone || done < plain0 || done >= plain1) process(std::true_type{}, st, blk0 + done, gone);
+      else process(std::false_type{}, st, blk0 + done, false);
       __syncwarp();
-      if (issued < steps) issue(issued++);
+      if (issued < count) issue(issued++);
       if ((done & 15) == 15) centre();
     }
+    turn = turn0 + count;
     centre();
     if (!ok) {
       // a copy did not arrive in time: say so and wait, with the same limit,
@@ -904,14 +897,14 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         abort_flag = 1;
         for (int i = done; i < issued; ++i) {
           int never = 0;
-          mbar_wait(&bars[i % STAGES], (phases >> (i % STAGES)) & 1u, &never);
+          mbar_wait(&bars[(turn0 + i) % STAGES], ((turn0 + i) / STAGES) & 1, &never);
         }
       }
       __syncwarp();
     }
 
     // ---- the end of the segment, or of this run's part of it
-    const float back = __uint_as_float(static_cast<uint32_t>(e_run == 0 ? 127 : e_run + 1) << 23);   // 1 / vf
+    const float back = 1.f / vf;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -921,14 +914,40 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         v += __shfl_xor_sync(0xffffffffu, v, 8);
         v += __shfl_xor_sync(0xffffffffu, v, 16);
         l[nt][c] = v;
+        if (!(seen >> (2 * nt + c) & 1u)) m[nt][c] = kKvFloor;
       }
     // the four channels of m tiles mt and mt + 1 that this lane holds of a row
     auto channel = [&](int mt) { return 2 * mt / (F::G / 8) * F::G + gr * (F::G / 8) + 2 * mt % (F::G / 8); };
     auto four = [&](int mt, int nt, int c) {
       return make_float4(o[mt][nt][c] * back, o[mt][nt][c + 2] * back, o[mt + 1][nt][c] * back, o[mt + 1][nt][c + 2] * back);
     };
+    if (count == seg.blocks && !together) {     // the whole segment
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int64_t at = row_y[8 * nt + 2 * tq + c];
+          if (at >= 0) {
+#pragma unroll
+            for (int mt = 0; mt < MT; mt += 2) kv_store_row<HD>(a, at, seg.h, channel(mt), four(mt, nt, c), l[nt][c]);
+          }
+        }
+      __syncwarp();                             // row_y is written again by the next segment
+      continue;
+    }
+
+    // a partial result: a run's in its first place if the segment began in
+    // an earlier run, else in its second; a thread block's in its first run's
+    // first
+    const int64_t end = x + left;               // the segment's last unit + 1
+    const KvParts parts(runs, end - seg.blocks - OV, end, OV, W);
+    auto slot_of = [&](int r) {
+      return a.part + (2 * static_cast<int64_t>(r) + (r == parts.first && !parts.merged(r) ? 1 : 0)) * A::SLOT;
+    };
+    const int mine = together ? static_cast<int>(blockIdx.x) * W : run;
+    float* slot = slot_of(mine);
     if (together) {
-      __syncthreads();                          // every warp is done with its ring
+      __syncthreads();                          // every warp is done with its region
       float* buf = reinterpret_cast<float*>(smem);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -944,10 +963,6 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
             *reinterpret_cast<float4*>(buf + (warp * ROWS + r) * A::LDO + channel(mt)) = four(mt, nt, c);
         }
       __syncthreads();
-      // the block's results go to its first warp's slot; the block has the
-      // whole segment if its runs do
-      const int64_t first_run = static_cast<int64_t>(blockIdx.x) * W;
-      float* slot = a.part + 2 * first_run * A::SLOT;
       for (int i = tid; i < ROWS * (HD / 4); i += W * 32) {
         const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
         if (r0 + r >= R) continue;
@@ -966,26 +981,13 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           acc.z = fmaf(v.z, f, acc.z);
           acc.w = fmaf(v.w, f, acc.w);
         }
-        *reinterpret_cast<float4*>(slot + r * HD + ch) = acc;
+        __stcg(reinterpret_cast<float4*>(slot + r * HD + ch), acc);
         if (ch == 0) {
-          slot[ROWS * HD + r] = mx;
-          slot[ROWS * HD + ROWS + r] = sum;
+          __stcg(slot + ROWS * HD + r, mx);
+          __stcg(slot + ROWS * (HD + 1) + r, sum);
         }
       }
-    } else if (whole) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int r = r0 + 8 * nt + 2 * tq + c;
-          if (r < R) {
-#pragma unroll
-            for (int mt = 0; mt < MT; mt += 2) kv_store_row<HD>(a, seg.row0, seg.h, r, channel(mt), four(mt, nt, c), l[nt][c]);
-          }
-        }
     } else {
-      // the run's first slot if the segment began in an earlier run
-      float* slot = a.part + (2 * run + (from > 0 ? 0 : 1)) * A::SLOT;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -993,93 +995,89 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           const int r = 8 * nt + 2 * tq + c;
           if (r0 + r < R) {
 #pragma unroll
-            for (int mt = 0; mt < MT; mt += 2)
-              *reinterpret_cast<float4*>(slot + r * HD + channel(mt)) = four(mt, nt, c);
+            for (int mt = 0; mt < MT; mt += 2) __stcg(reinterpret_cast<float4*>(slot + r * HD + channel(mt)), four(mt, nt, c));
             if (gr == 0) {
-              slot[ROWS * HD + r] = m[nt][c];
-              slot[ROWS * HD + ROWS + r] = l[nt][c];
+              __stcg(slot + ROWS * HD + r, m[nt][c]);
+              __stcg(slot + ROWS * (HD + 1) + r, l[nt][c]);
             }
           }
         }
     }
-    if (lane == 0 && from == 0 && count > 0 && !whole) {
-      // the run that holds the segment's last block: the last i with i total / runs <= its place
-      const int64_t last = x + left - 1;
-      meta[0] = make_int4(static_cast<int>(((last + 1) * runs - 1) / total), seg.row0, seg.h, r0);
-      meta[1] = make_int4(R, 0, 0, 0);
-    }
-  }
-}
 
-// Merges the partial results of the segments that began in the runs of
-// thread block blockIdx.x and went on into later runs.  A block takes one
-// row of each; its threads are the float4 channels of the row times slices
-// of the contributing thread blocks, summed per slice and then over the
-// slices, always in the same order.
-constexpr int kKvJoinThreads = 256;
-template <int HD, int ROWS, int W>
-__global__ void __launch_bounds__(kKvJoinThreads) kv_join_kernel(const KvAttentionArgs a) {
-  constexpr int SLOT = ROWS * (HD + 2), LANES = HD / 4, SLICES = kKvJoinThreads / LANES;
-  __shared__ float4 acc_s[SLICES][LANES];
-  __shared__ float sum_s[SLICES], max_s[SLICES];
-  allow_dependents_launch();
-  grid_dependency_wait();
-  const int slice = threadIdx.x / LANES, in = threadIdx.x % LANES, ch = in * 4, r = blockIdx.y;
-  for (int w = 0; w < W; ++w) {
-    const int first = blockIdx.x * W + w;
-    const int4 m0 = a.meta[2 * first];
-    if (m0.x < 0) continue;
-    const int R = a.meta[2 * first + 1].x;
-    const int last = m0.x, row0 = m0.y, h = m0.z, r0 = m0.w;
-    if (r0 + r >= R) continue;
-    float mx = kKvFloor, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float* slot) {
-      const float4 v = *reinterpret_cast<const float4*>(slot + r * HD + ch);
-      const float mk = slot[ROWS * HD + r], lk = slot[ROWS * HD + ROWS + r];
-      const float m_new = fmaxf(mx, mk);
-      const float f = kv_exp2(mx - m_new), fk = kv_exp2(mk - m_new);
-      mx = m_new;
-      sum = fmaf(lk, fk, sum * f);
-      acc.x = fmaf(v.x, fk, acc.x * f);
-      acc.y = fmaf(v.y, fk, acc.y * f);
-      acc.z = fmaf(v.z, fk, acc.z * f);
-      acc.w = fmaf(v.w, fk, acc.w * f);
+    // ---- tickets: the last of a group merges it, the last group the segment
+    const int width = together ? W * 32 : 32, me = together ? tid : lane;
+    // whether this was the last of n arrivals; the counter is left at zero
+    auto arrive = [&](uint32_t* counter, int n) -> bool {
+      if (together) __syncthreads(); else __syncwarp();   // all of the result is written
+      int last = 0;
+      if (me == 0) {
+        __threadfence();
+        last = atomicAdd(counter, 1u) == static_cast<uint32_t>(n - 1);
+        if (last) {
+          *counter = 0;
+          __threadfence();
+        }
+      }
+      if (!together) return __shfl_sync(0xffffffffu, last, 0) != 0;
+      if (tid == 0) last_flag = last;
+      __syncthreads();
+      last = last_flag;
+      __syncthreads();
+      return last != 0;
     };
+    // merges results k0, k0 + step, ... below k1: their own, or (step > 1)
+    // their groups'; into Y, or as a group into the place of the first
+    auto merge = [&](int k0, int k1, int step, bool whole) {
+      const int mls = ROWS * (step > 1 ? HD + 2 : HD);
+      for (int i = me; i < ROWS * (HD / 4); i += width) {
+        const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
+        if (r0 + r >= R) continue;
+        float mx = kKvFloor, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = first / W + slice; k <= last / W; k += SLICES) {
-      if (a.together[k]) {
-        add(a.part + 2 * static_cast<int64_t>(k) * W * SLOT);
-      } else {
-        const int lo = max(first, k * W), hi = min(last, k * W + W - 1);
-        for (int q = lo; q <= hi; ++q) add(a.part + (2 * static_cast<int64_t>(q) + (q == first ? 1 : 0)) * SLOT);
+        for (int k = k0; k < k1; k += step) {
+          const float* p = slot_of(parts.run(k));
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p + r * HD + ch));
+          const float mk = __ldcg(p + mls + r), lk = __ldcg(p + mls + ROWS + r);
+          const float m_new = fmaxf(mx, mk);
+          const float f = kv_exp2(mx - m_new), fk = kv_exp2(mk - m_new);
+          mx = m_new;
+          sum = fmaf(lk, fk, sum * f);
+          acc.x = fmaf(v.x, fk, acc.x * f);
+          acc.y = fmaf(v.y, fk, acc.y * f);
+          acc.z = fmaf(v.z, fk, acc.z * f);
+          acc.w = fmaf(v.w, fk, acc.w * f);
+        }
+        if (whole) {
+          const int rr = r0 + r, i_new = rr / a.per;
+          const int64_t row = static_cast<int64_t>(seg.row0 + i_new) * a.heads + seg.h * a.per + rr - i_new * a.per;
+          kv_store_row<HD>(a, row * HD, seg.h, ch, acc, sum);
+        } else {
+          float* p = slot_of(parts.run(k0));
+          __stcg(reinterpret_cast<float4*>(p + r * HD + ch), acc);   // read by this thread alone
+          if (ch == 0) {
+            __stcg(p + ROWS * (HD + 2) + r, mx);
+            __stcg(p + ROWS * (HD + 3) + r, sum);
+          }
+        }
       }
+    };
+    constexpr int kGroup = 8;
+    int group = parts.n;                        // results of a group: about the root of all
+    if (parts.n > kGroup)
+      for (group = kGroup; group * group < parts.n;) ++group;
+    const int groups = (parts.n + group - 1) / group;
+    bool last = true;
+    if (groups > 1) {
+      const int k0 = parts.index(mine) / group * group, of = min(group, parts.n - k0);
+      // (a group of one may share its ticket with the next segment's first: it takes none)
+      if (of > 1) last = arrive(a.tickets + gridDim.x * W + parts.run(k0), of);
+      else if (together) __syncthreads();
+      else __syncwarp();
+      if (last) merge(k0, k0 + of, 1, false);
     }
-    acc_s[slice][in] = acc;
-    if (in == 0) {
-      sum_s[slice] = sum;
-      max_s[slice] = mx;
-    }
-    __syncthreads();
-    if (slice == 0) {
-      float top = max_s[0];
-#pragma unroll
-      for (int k = 1; k < SLICES; ++k) top = fmaxf(top, max_s[k]);
-      sum = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < SLICES; ++k) {
-        const float f = kv_exp2(max_s[k] - top);
-        const float4 v = acc_s[k][in];
-        sum = fmaf(sum_s[k], f, sum);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
-      }
-      kv_store_row<HD>(a, row0, h, r0 + r, ch, acc, sum);
-    }
-    __syncthreads();
+    if (last && arrive(a.tickets + parts.first, groups > 1 ? groups : parts.n))
+      merge(0, parts.n, groups > 1 ? group : 1, true);
   }
 }
 
@@ -1144,8 +1142,6 @@ cudaError_t kv_attention_launch(const KvAttentionArgs& a, int bits, int group, c
       set.fetch_or(bit, std::memory_order_relaxed);
     }
     e = launch_kernel(kernel, dim3(p.grid), dim3(A::W * 32), smem, stream, true, a);
-    if (e != cudaSuccess) return;
-    e = launch_kernel(kv_join_kernel<HD, A::ROWS, A::W>, dim3(p.grid, A::ROWS), dim3(kKvJoinThreads), 0, stream, true, a);
   });
   return e;
 }

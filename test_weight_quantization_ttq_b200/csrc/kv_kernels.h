@@ -70,8 +70,7 @@ struct KvAttentionArgs {
   const uint64_t* tree = nullptr;
   void* Y = nullptr;
   float* part = nullptr;        // two partial results per warp of the grid
-  int4* meta = nullptr;         // two words of 16 bytes per warp: the cut segment that began in its run
-  int* together = nullptr;      // per block: its warps' partial results are merged in its first slot
+  uint32_t* tickets = nullptr;  // two per warp of the grid, zero before and after
 };
 // How a launch is laid out: 8 nt query rows per tile, `grid` blocks of
 // kKvAttentionWarps warps, the floats of one partial result, and the bytes
@@ -79,8 +78,7 @@ struct KvAttentionArgs {
 constexpr int kKvAttentionWarps = 4;
 struct KvAttentionPlan {
   int nt, grid;
-  int64_t slot_floats;
-  int64_t meta_bytes, together_bytes, part_bytes;
+  int64_t slot_floats, part_bytes;
 };
 // grid 0: the format is not built.
 KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows);
