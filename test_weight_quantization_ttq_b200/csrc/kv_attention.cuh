@@ -64,7 +64,9 @@ struct KvAttention {
   static constexpr int KS = HD / 16;                // k steps of the first product
   static constexpr int MT = HD / 16;                // m tiles of the second
   static constexpr int QFRAG = NT * KS * 32 * 8;    // a warp's Q fragments
-  static constexpr int ROWINFO = ROWS * (24 + 8 * NG);   // and what it knows of its rows
+  static constexpr int ROWINFO = ROWS * (16 + 8 * NG);   // and what it knows of its rows
+  static constexpr int LDO = HD + 4;                // padded row of the accumulators in shared memory
+  static constexpr int TILE = ROWS * LDO * 4;       // their bytes
   // whether V's codes are taken raw and their zeros off the sums (see above)
   static constexpr bool VRAW = BITS != 8 && NT == 1 && NG <= 2;
   // what even and odd fields of a half word are offset by
@@ -78,12 +80,14 @@ struct KvAttention {
   static constexpr int CTAS = BY_REGS >= 4 && room(4) >= 2 * F::BLOCK ? 4 : BY_REGS >= 3 && room(3) >= 2 * F::BLOCK ? 3 : 2;
   static constexpr int STAGES = room(CTAS) >= 4 * F::BLOCK ? 4 : 2;
   static_assert(room(CTAS) >= 2 * F::BLOCK, "the ring needs two stages");
-  static constexpr int WARP_BYTES = STAGES * F::BLOCK + QFRAG + ROWINFO;
-  static constexpr int LDO = HD + 4;                // padded row of the merge buffer
-  static constexpr int MERGE = W * ROWS * LDO * 4;
-  // dynamic shared memory: the warps' regions (in the end the merge buffer),
-  // then 16 bytes a sequence
-  static constexpr int SMEM = W * WARP_BYTES > MERGE ? W * WARP_BYTES : MERGE;
+  // a warp's region: ring, Q fragments, row information; at a segment's end
+  // its accumulators, then the weights of the results that it merges
+  static constexpr int REGION = STAGES * F::BLOCK + QFRAG + ROWINFO;
+  static constexpr int WARP_BYTES = REGION > TILE ? REGION : TILE;
+  static constexpr int MOST = 25;                   // results (or groups of results) merged at a time
+  static_assert((MOST * (2 * ROWS + 1) + ROWS) * 4 <= STAGES * F::BLOCK + QFRAG, "weights fit the region");
+  // dynamic shared memory: the warps' regions, then 16 bytes a sequence
+  static constexpr int SMEM = W * WARP_BYTES;
   // a partial result: accumulators, m and l, m and l of the group merged here
   static constexpr int SLOT = ROWS * (HD + 4);
   // what a segment costs besides its blocks, in blocks: its rows of Q, the
@@ -230,50 +234,40 @@ struct KvSegment {
   int blocks;            // and how many there are
 };
 
-// E (2, 4 or 8) consecutive elements of a row tensor of the given type.
-template <int E>
-__device__ __forceinline__ void kv_load_lane(const void* p, int type, int64_t at, float (&v)[E]) {
-  if (type == kRowF32) {
-    const float2* s = reinterpret_cast<const float2*>(static_cast<const float*>(p) + at);
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      const float2 f = s[e];
-      v[2 * e] = f.x, v[2 * e + 1] = f.y;
-    }
-    return;
-  }
-  uint32_t w[E / 2];
-  const uint16_t* s = static_cast<const uint16_t*>(p) + at;
-  if constexpr (E == 2) w[0] = *reinterpret_cast<const uint32_t*>(s);
-  if constexpr (E == 4) {
-    const uint2 u = *reinterpret_cast<const uint2*>(s);
+// N (1, 2, 4 or 8) consecutive words.
+template <int N>
+__device__ __forceinline__ void kv_load_words(const void* p, uint32_t* w) {
+  if constexpr (N == 1) {
+    w[0] = *static_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 u = *static_cast<const uint2*>(p);
     w[0] = u.x, w[1] = u.y;
-  }
-  if constexpr (E == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(s);
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-  }
+  } else {
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e) {
-    if (type == kRowBF16) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-    } else {
-      const float2 f = __half22float2(u32_as_h2(w[e]));
-      v[2 * e] = f.x, v[2 * e + 1] = f.y;
+    for (int i = 0; i < N; i += 4) {
+      const uint4 u = static_cast<const uint4*>(p)[i / 4];
+      w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
     }
   }
 }
+
 // Four consecutive elements, rounded to the type.
 __device__ __forceinline__ void kv_store4(void* p, int type, int64_t at, float4 v) {
-  if (type == kRowF32)
+  if (type == kRowF32) {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = v;
-  else if (type == kRowBF16)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) =
-        make_uint2(kv_pack2<kRowBF16>(v.x, v.y), kv_pack2<kRowBF16>(v.z, v.w));
-  else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) =
-        make_uint2(kv_pack2<kRowF16>(v.x, v.y), kv_pack2<kRowF16>(v.z, v.w));
+  } else {
+    const uint2 b = make_uint2(kv_pack2<kRowBF16>(v.x, v.y), kv_pack2<kRowBF16>(v.z, v.w));
+    const uint2 h = make_uint2(kv_pack2<kRowF16>(v.x, v.y), kv_pack2<kRowF16>(v.z, v.w));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) = type == kRowBF16 ? b : h;
+  }
+}
+
+// A float4 that other SMs wrote in this launch, past the L1 cache.
+__device__ __forceinline__ float4 kv_load_shared_result(const float* p) {
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
 }
 
 // Stores 4 channels of a row: O / l, times D_v^{-1/2}; at: the row's first
@@ -289,6 +283,14 @@ __device__ __forceinline__ void kv_store_row(const KvAttentionArgs& a, int64_t a
   kv_store4(a.Y, a.y_type, at + ch, o);
 }
 
+// a / b for a, b >= 0, by 32-bit division where both fit; the 64-bit one is
+// long, and out of line.
+static __device__ __noinline__ int64_t kv_div64(int64_t a, int64_t b) { return a / b; }
+__device__ __forceinline__ int64_t kv_div(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return kv_div64(a, b);
+}
+
 // How the units of work are cut into runs: run i is [start(i), start(i + 1)).
 struct KvRuns {
   int64_t total, each;
@@ -296,7 +298,7 @@ struct KvRuns {
   __device__ __forceinline__ int64_t start(int i) const { return i * each + min(i, more); }
   __device__ __forceinline__ int of(int64_t unit) const {
     const int64_t cut = more * (each + 1);
-    return static_cast<int>(unit < cut ? unit / (each + 1) : more + (unit - cut) / each);
+    return static_cast<int>(unit < cut ? kv_div(unit, each + 1) : more + kv_div(unit - cut, each));
   }
 };
 
@@ -306,9 +308,10 @@ struct KvRuns {
 struct KvParts {
   int first, last, block0, block1, W, n;
   __device__ __forceinline__ KvParts(const KvRuns& r, int64_t begin, int64_t end, int overhead, int warps) : W(warps) {
-    first = r.of(begin + overhead);
-    last = r.of(end - 1);
     int lo = r.of(begin);
+    first = lo;
+    while (r.start(first + 1) <= begin + overhead) ++first;
+    last = r.of(end - 1);
     if (r.start(lo) != begin) ++lo;                 // the first run wholly in the segment
     const int hi = r.start(last + 1) == end ? last + 1 : last;
     block0 = (lo + W - 1) / W;
@@ -355,8 +358,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
   uint8_t* ring = smem + warp * A::WARP_BYTES;
   uint32_t* qfrag = reinterpret_cast<uint32_t*>(ring + STAGES * F::BLOCK);
   uint64_t* row_mask = reinterpret_cast<uint64_t*>(ring + STAGES * F::BLOCK + A::QFRAG);
-  int64_t* row_y = reinterpret_cast<int64_t*>(row_mask + ROWS);  // the row's first element in Y; -1: not there
-  float* q_factor = reinterpret_cast<float*>(row_y + ROWS);      // t = <row, (c - z) s> * q_factor
+  float* q_factor = reinterpret_cast<float*>(row_mask + ROWS);   // t = <row, (c - z) s> * q_factor
   int* row_pos = reinterpret_cast<int*>(q_factor + ROWS);
   float* q_sum = reinterpret_cast<float*>(row_pos + ROWS);       // [NG][ROWS] sums of a row's group
   float* q_off = q_sum + NG * ROWS;                              // the same with the fields' offsets as weights
@@ -409,11 +411,11 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       base += __shfl_sync(0xffffffffu, v, 31);
     }
     if (lane == 0) {
-      const int64_t total = base * g.kv_heads, most = (total + A::LEAST - 1) / A::LEAST;
+      const int64_t total = base * g.kv_heads, most = kv_div(total + A::LEAST - 1, A::LEAST);
       const int all = static_cast<int>(gridDim.x) * W, runs = most < all ? static_cast<int>(most) : all;
       runs_s.total = total;
       runs_s.runs = runs;
-      runs_s.each = runs > 0 ? total / runs : 0;
+      runs_s.each = runs > 0 ? kv_div(total, runs) : 0;
       runs_s.more = static_cast<int>(total - runs_s.each * runs);
     }
   }
@@ -438,7 +440,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     tiles = tiles_of(seg.n);
   };
   if (x < x1) {
-    const int64_t per_head_x = x / g.kv_heads;
+    const int64_t per_head_x = kv_div(x, g.kv_heads);
     int lo = 0, hi = g.batch - 1;               // first b with end * kv_heads > x
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     }
     enter(lo);
     const int64_t rest = x - (lo > 0 ? end_of(seqs[lo - 1]) * g.kv_heads : 0);
-    const int64_t units = seg.blocks + OV, tile = rest / units;
+    const int64_t units = seg.blocks + OV, tile = kv_div(rest, units);
     left = units - (rest - tile * units);
     seg.h = static_cast<int>(tile) / tiles;
     seg.tile = static_cast<int>(tile) - seg.h * tiles;
@@ -481,25 +483,52 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     // whose warps merge theirs it goes on without blocks)
     if (count == 0 && !together) continue;
 
+    // ---- the tile's rows: their loads from Q are on their way while the
+    // pages are looked up and the copies start
+    constexpr int E = HD / 32;                  // consecutive channels of a lane
+    const int here = min(R - r0, ROWS);         // rows of the tile
+    int64_t q_at = 0;                           // row `lane` of the tile in Q
+    if (lane < ROWS) {
+      const int rr = min(r0 + lane, R - 1), i_new = rr / a.per, head = seg.h * a.per + rr - i_new * a.per;
+      const int64_t row = seg.row0 + i_new;
+      q_at = row * a.q_row + head * a.q_head;
+      uint64_t mask = a.tree != nullptr ? a.tree[row] : (2ull << i_new) - 1ull;
+      row_mask[lane] = mask;
+      row_pos[lane] = old + __popcll(mask & ~(1ull << i_new));
+    }
+    uint32_t raw[8][E] = {};                    // E words of float32, E / 2 of 16-bit elements
+    auto load_rows = [&](int nt) {
+      const bool wide = a.q_type == kRowF32;
+      const uint8_t* q = static_cast<const uint8_t*>(a.Q) + lane * (wide ? 4 * E : 2 * E);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t at = __shfl_sync(0xffffffffu, q_at, nt * 8 + k);   // (rows that are not there: the last one)
+        if (wide) kv_load_words<E>(q + at * 4, raw[k]);
+        else kv_load_words<E / 2>(q + at * 2, raw[k]);
+      }
+    };
+    load_rows(0);
+
     // ---- start the copies
     const int blk0 = seg.first + from;          // this run's first block of the segment
     const uint8_t* src = nullptr;               // this lane's block 32 k + lane
     bool any_absent = false;
     const int turn0 = turn;
-    auto issue = [&](int i) {                   // by the whole warp; one lane does it
-      if ((i & 31) == 0) {
-        const int j = i + lane, blk = blk0 + j;
-        src = nullptr;
-        if (j < count) {
-          const int pg = blk / g.page_blocks, page = g.table[seg.b * g.table_stride + pg];
-          if (page >= 0 && page < g.num_pages)
-            src = g.pages + page * g.page_bytes +
-                  (static_cast<int64_t>(seg.h) * g.page_blocks + (blk - pg * g.page_blocks)) * F::BLOCK;
-          else
-            set_flag(g.status, TTQ_FLAG_BAD_INDEX);
-        }
-        any_absent = __any_sync(0xffffffffu, j < count && src == nullptr) || any_absent;
+    auto look_up = [&](int i) {                 // blocks i to i + 31
+      const int j = i + lane, blk = blk0 + j;
+      src = nullptr;
+      if (j < count) {
+        const int pg = static_cast<int>(static_cast<uint64_t>(blk) * a.page_magic >> 40);   // blk / page_blocks
+        const int page = g.table[seg.b * g.table_stride + pg];
+        if (page >= 0 && page < g.num_pages)
+          src = g.pages + page * g.page_bytes +
+                (static_cast<int64_t>(seg.h) * g.page_blocks + (blk - pg * g.page_blocks)) * F::BLOCK;
+        else
+          set_flag(g.status, TTQ_FLAG_BAD_INDEX);
       }
+      any_absent = __any_sync(0xffffffffu, j < count && src == nullptr) || any_absent;
+    };
+    auto issue = [&](int i) {                   // by the whole warp; one lane does it
       if (lane == (i & 31)) {
         const int s = (turn0 + i) % STAGES;
         absent[s] = src == nullptr;
@@ -512,82 +541,69 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       }
     };
     int issued = 0;
-    for (; issued < STAGES && issued < count; ++issued) issue(issued);
+    look_up(0);
+#pragma unroll
+    for (; issued < STAGES; ++issued)
+      if (issued < count) issue(issued);
 
-    // ---- the tile's rows of Q as B fragments, and what each row sees
+    // ---- the rows as B fragments: scaled by a power of two to [1, 2) and
+    // rounded; rows that are not there are zero
     {
-      constexpr int E = HD / 32;                // consecutive channels of a lane
-      int64_t q_at = -1;                        // row `lane` of the tile in Q
-      if (lane < ROWS) {
-        const int rr = r0 + lane, i_new = rr / a.per, head = seg.h * a.per + rr - i_new * a.per;
-        const int64_t row = seg.row0 + i_new;
-        uint64_t mask = 0;
-        if (rr < R) {
-          q_at = row * a.q_row + head * a.q_head;
-          mask = a.tree != nullptr ? a.tree[row] : (2ull << i_new) - 1ull;
-        }
-        row_y[lane] = rr < R ? (row * a.heads + head) * HD : -1;
-        row_mask[lane] = mask;
-        row_pos[lane] = old + __popcll(mask & ~(1ull << (i_new & 63)));
-      }
       float dk[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) dk[e] = a.Dk != nullptr ? __ldg(a.Dk + seg.h * HD + lane * E + e) : 1.f;
-#pragma unroll
+      const float factor = a.scale * (a.cap > 0.f ? kv_rcp(a.cap) : kKvLog2e);
+#pragma unroll 1
       for (int nt = 0; nt < NT; ++nt) {
-        float v[8][E];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int64_t at = __shfl_sync(0xffffffffu, q_at, nt * 8 + k);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[k][e] = 0.f;
-          if (at >= 0) kv_load_lane<E>(a.Q, a.q_type, at + lane * E, v[k]);
-        }
+        if (nt > 0) load_rows(nt);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int r = nt * 8 + k;
-          float big = 0.f;
+          float v[E], big = 0.f;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            v[k][e] *= dk[e];
-            big = fmaxf(big, fabsf(v[k][e]));
+            const uint32_t w = raw[k][e / 2];
+            const float bf = __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
+            const float hf = __half2float(e & 1 ? u32_as_h2(w).y : u32_as_h2(w).x);
+            const float x = a.q_type == kRowF32 ? __uint_as_float(raw[k][e]) : a.q_type == kRowBF16 ? bf : hf;
+            v[e] = r < here ? x * dk[e] : 0.f;
+            big = fmaxf(big, fabsf(v[e]));
           }
           // the row's largest magnitude: bits of non-negative floats order as integers
           const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
           const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
           const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^-(ex - 127)
-          const float up = __uint_as_float(static_cast<uint32_t>(ex) << 23);
 #pragma unroll
           for (int e = 0; e < E; e += 2) {
             const int c = lane * E + e, kg = c / F::G, j = c % F::G;
             const int quarter = j / (F::G / 4), idx = kg * (F::G / 4) + j % (F::G / 4);
             qfrag[((nt * KS + idx / 4) * 32 + 4 * k + quarter) * 2 + (idx % 4) / 2] =
-                h2_as_u32(__floats2half2_rn(v[k][e] * down, v[k][e + 1] * down));
+                h2_as_u32(__floats2half2_rn(v[e] * down, v[e + 1] * down));
           }
-          if (lane == 0) q_factor[r] = a.scale * up * (a.cap > 0.f ? 1.f / a.cap : kKvLog2e);
+          if (lane == 0)
+            q_factor[r] = factor * __uint_as_float(static_cast<uint32_t>(ex) << 23);
         }
       }
       __syncwarp();
       if constexpr (BITS != 8) {
         // the sums of each group of the rounded rows: the first product with
         // ones, and (INT2, whose fields' offsets differ) with the offsets, as codes
+#pragma unroll 1
+        for (int kn = 0; kn < NG * NT; ++kn) {
+          const int k = kn / NT, nt = kn % NT;
+          float one[4] = {}, off[4] = {};
 #pragma unroll
-        for (int k = 0; k < NG; ++k)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float one[4] = {}, off[4] = {};
-#pragma unroll
-            for (int j = 0; j < KS / NG; ++j) {
-              const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * KS + k * (KS / NG) + j) * 32 + lane) * 2);
-              kv_mma(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, bq.x, bq.y);
-              if constexpr (BITS == 2) kv_mma(off, A::EVEN, A::EVEN, A::ODD, A::ODD, bq.x, bq.y);
-            }
-            if (gr == 0) {
-              *reinterpret_cast<float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq) = make_float2(one[0], one[1]);
-              if constexpr (BITS == 2)
-                *reinterpret_cast<float2*>(q_off + k * ROWS + 8 * nt + 2 * tq) = make_float2(off[0], off[1]);
-            }
+          for (int j = 0; j < KS / NG; ++j) {
+            const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * KS + k * (KS / NG) + j) * 32 + lane) * 2);
+            kv_mma(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, bq.x, bq.y);
+            if constexpr (BITS == 2) kv_mma(off, A::EVEN, A::EVEN, A::ODD, A::ODD, bq.x, bq.y);
           }
+          if (gr == 0) {
+            *reinterpret_cast<float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq) = make_float2(one[0], one[1]);
+            if constexpr (BITS == 2)
+              *reinterpret_cast<float2*>(q_off + k * ROWS + 8 * nt + 2 * tq) = make_float2(off[0], off[1]);
+          }
+        }
         __syncwarp();
       }
     }
@@ -600,32 +616,6 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     bool all_seen = false;                      // all columns of all lanes
     float vf = 1.2676506e30f;                   // 2^-E; at first 2^100, so that any scale lowers it
     float zs[A::VRAW ? NG : 1][4] = {};         // sums of p s (offset + z) 2^-E per group
-    // takes the offsets and zeros off the accumulators, often enough that the
-    // sums of offset codes do not grow much past their difference
-    auto centre = [&]() {
-      if constexpr (A::VRAW) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[mt][0][i] -= zs[mt / (MT / NG)][i];
-#pragma unroll
-        for (int k = 0; k < NG; ++k) zs[k][0] = zs[k][1] = zs[k][2] = zs[k][3] = 0.f;
-      }
-    };
-    auto rescale = [&](int nt, int c, float f) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        o[mt][nt][c] *= f;
-        o[mt][nt][c + 2] *= f;
-      }
-      if constexpr (A::VRAW) {
-#pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          zs[k][c] *= f;
-          zs[k][c + 2] *= f;
-        }
-      }
-    };
     // blocks [plain0, plain1) need no masks: not those that the window of the
     // last new token does not cover, nor those that reach the new tokens
     int plain0 = 0;
@@ -636,8 +626,28 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     }
     const int plain1 = (old >> 4) - blk0;                             // blocks before the new tokens
 
-    auto process = [&](auto masked_c, uint32_t st, int blk, bool gone) {
-      constexpr bool MASKED = decltype(masked_c)::value;
+#pragma unroll 1
+    for (int done = 0; done < count; ++done) {
+      const int stage = (turn0 + done) % STAGES, blk = blk0 + done;
+      if (!mbar_wait(&bars[stage], ((turn0 + done) / STAGES) & 1, &abort_flag)) {
+        // a copy did not arrive in time: say so and wait, with the same limit,
+        // for the copies still in flight; the run ends here
+        ok = false;
+        if (lane == 0) {
+          set_flag(g.status, TTQ_FLAG_TIMEOUT);
+          abort_flag = 1;
+#pragma unroll 1
+          for (int i = done; i < min(issued, count); ++i) {
+            int never = 0;
+            mbar_wait(&bars[(turn0 + i) % STAGES], ((turn0 + i) / STAGES) & 1, &never);
+          }
+        }
+        __syncwarp();
+        break;
+      }
+      const uint32_t st = smem_addr(ring + stage * F::BLOCK);
+      const bool gone = any_absent && absent[stage] != 0;
+      const bool masked = gone || done < plain0 || done >= plain1;
       // -- scores
       float s[NT][4];
       uint32_t kp[2][NG];
@@ -697,23 +707,25 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           }
         }
       }
-      // -- V's scales of tokens gr and gr + 8; tokens that are not there count
-      // for nothing
-      const int there = MASKED ? (gone ? 0 : seg.kv - blk * 16) : 16;   // tokens of the block
+      // -- V's scales of tokens gr and gr + 8, and zeros of 2 tq, 2 tq + 1 (+ 8)
       float vs[2][NG];
-      bool higher = !all_seen;                  // a scale or a score is well above the running ones
+      [[maybe_unused]] uint32_t vz[2][NG], keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      const uint32_t vst = st + F::V_OFFSET;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         uint32_t vp[NG];
-        kv_lds<NG>(st + F::V_OFFSET + F::CODES + (gr + 8 * r) * NG * 4, vp);
+        kv_lds<NG>(vst + F::CODES + (gr + 8 * r) * NG * 4, vp);
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          vs[r][k] = __half2float(u32_as_h2(vp[k]).x);
-          if (MASKED && gr + 8 * r >= there) vs[r][k] = 0.f;
-          higher |= vs[r][k] * vf > 64.f;
+        for (int k = 0; k < NG; ++k) vs[r][k] = __half2float(u32_as_h2(vp[k]).x);
+        if constexpr (BITS != 8) {
+          uint32_t e[2 * NG];                   // both tokens' pairs are contiguous
+          kv_lds<NG == 1 ? 2 : 4>(vst + F::CODES + (2 * tq + 8 * r) * NG * 4, e);
+          if constexpr (NG == 4) kv_lds<4>(vst + F::CODES + (2 * tq + 8 * r) * NG * 4 + 16, e + 4);
+#pragma unroll
+          for (int k = 0; k < NG; ++k) vz[r][k] = __byte_perm(e[k], e[NG + k], 0x7632);
         }
       }
-      // -- scores in powers of two less the running maximum, masks
+      // -- scores in powers of two less the running maximum
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float2 f = *reinterpret_cast<const float2*>(q_factor + 8 * nt + 2 * tq);
@@ -727,26 +739,58 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[nt][i] = fmaf(s[nt][i], (i & 1) ? f.y : f.x, -m[nt][i & 1]);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (MASKED) {
-            const int j = (i & 2) ? gr + 8 : gr, p = blk * 16 + j, row = 8 * nt + 2 * tq + (i & 1);
-            bool see = j < there;
-            if (see && p >= old) {
-              see = (row_mask[row] >> (p - old)) & 1ull;
-              if (see && a.window > 0) {
-                const int k_new = p - old;
-                const uint64_t mask = a.tree != nullptr ? a.tree[seg.row0 + k_new] : (2ull << k_new) - 1ull;
-                see = row_pos[row] - old - __popcll(mask & ~(1ull << k_new)) < a.window;
-              }
-            } else if (see && a.window > 0) {
-              see = row_pos[row] - p < a.window;
+      }
+      // -- masks: lane r finds which of the block's tokens row r sees; tokens
+      // that are not there count for nothing, whatever their bytes are
+      if (masked) {
+        const int p0 = blk * 16, there = gone ? 0 : min(seg.kv - p0, 16), j0 = old - p0;
+        auto below = [](int64_t n) { return n <= 0 ? 0u : n >= 16 ? 0xFFFFu : (1u << n) - 1u; };
+        const uint64_t mask = row_mask[lane % ROWS];
+        const int pos = row_pos[lane % ROWS];
+        uint32_t before = below(j0), since = 0;   // of the old tokens, of the new ones
+        if (j0 < 16) since = static_cast<uint32_t>(j0 >= 0 ? mask << j0 : mask >> min(-j0, 63)) & ~below(j0);
+        if (a.window > 0) {
+          const uint32_t far = below(pos - a.window + 1 - p0);
+          before &= ~far;
+          if (a.tree == nullptr) {
+            since &= ~far;
+          } else {
+#pragma unroll 1
+            for (int j = max(j0, 0); j < there; ++j) {
+              const int k_new = j - j0;
+              if (pos - old - __popcll(a.tree[seg.row0 + k_new] & ~(1ull << k_new)) >= a.window) since &= ~(1u << j);
             }
-            if (!see) s[nt][i] = -INFINITY;
           }
-          higher |= s[nt][i] > kKvSlack;
+        }
+        const uint32_t vis = (before | since) & below(there);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t v = __shfl_sync(0xffffffffu, vis, 8 * nt + 2 * tq + c) >> gr;
+            if (!(v & 1u)) s[nt][c] = -INFINITY;
+            if (!(v & 256u)) s[nt][c + 2] = -INFINITY;
+          }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int t0 = 2 * tq + 8 * r;
+          keep[r] = (t0 < there ? 0xFFFFu : 0u) | (t0 + 1 < there ? 0xFFFF0000u : 0u);
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            if (gr + 8 * r >= there) vs[r][k] = 0.f;
+            if constexpr (BITS != 8) vz[r][k] &= keep[r];
+          }
         }
       }
+      bool higher = !all_seen;                  // a scale or a score is well above the running ones
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int k = 0; k < NG; ++k) higher |= vs[r][k] * vf > 64.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) higher |= s[nt][i] > kKvSlack;
       // -- the running maxima move only then (and to a column's first score)
       if (__any_sync(0xffffffffu, higher)) {
         float top = 0.f;                        // the largest scale (NaN aside)
@@ -773,12 +817,24 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
             if (!(up > -INFINITY) || ((seen & bit) && up <= kKvSlack)) up = 0.f;
             else seen |= bit;
             // (before the first score l and o are zero, or NaN)
-            const float f = up < 0.f ? 1.f : kv_exp2(-up);
+            float f = up < 0.f ? 1.f : kv_exp2(-up);
             m[nt][c] += up;
             s[nt][c] -= up;
             s[nt][c + 2] -= up;
             l[nt][c] *= f;
-            rescale(nt, c, f * fv);
+            f *= fv;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              o[mt][nt][c] *= f;
+              o[mt][nt][c + 2] *= f;
+            }
+            if constexpr (A::VRAW) {
+#pragma unroll
+              for (int k = 0; k < NG; ++k) {
+                zs[k][c] *= f;
+                zs[k][c + 2] *= f;
+              }
+            }
           }
         all_seen = __all_sync(0xffffffffu, seen == ALL);
       }
@@ -792,25 +848,6 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       // -- p s_V 2^-E as the B operand, and the second product
       constexpr int MTG = MT / NG;              // m tiles of a group
       constexpr int MTW = BITS == 8 ? 1 : 16 / BITS / 2;   // m tiles of a word
-      const uint32_t vst = st + F::V_OFFSET;
-      [[maybe_unused]] uint32_t vz[2][NG], keep[2] = {};   // zeros of tokens 2 tq, 2 tq + 1 (+ 8)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if constexpr (MASKED) {
-          const int t0 = 2 * tq + 8 * r;
-          keep[r] = (t0 < there ? 0xFFFFu : 0u) | (t0 + 1 < there ? 0xFFFF0000u : 0u);
-        }
-        if constexpr (BITS != 8) {
-          uint32_t e[2 * NG];                   // both tokens' pairs are contiguous
-          kv_lds<NG == 1 ? 2 : 4>(vst + F::CODES + (2 * tq + 8 * r) * NG * 4, e);
-          if constexpr (NG == 4) kv_lds<4>(vst + F::CODES + (2 * tq + 8 * r) * NG * 4 + 16, e + 4);
-#pragma unroll
-          for (int k = 0; k < NG; ++k) {
-            vz[r][k] = __byte_perm(e[k], e[NG + k], 0x7632);
-            if constexpr (MASKED) vz[r][k] &= keep[r];
-          }
-        }
-      }
       uint32_t vw[2][PW], pv[2][BITS == 8 ? 2 : 16 / BITS];
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
@@ -819,7 +856,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float w0 = s[nt][0] * s0, w1 = s[nt][1] * s0, w2 = s[nt][2] * s1, w3 = s[nt][3] * s1;
-          if constexpr (MASKED) {               // a NaN scale reaches only those that see its token
+          if (masked) {                         // a NaN scale reaches only those that see its token
             w0 = s[nt][0] == 0.f ? 0.f : w0;
             w1 = s[nt][1] == 0.f ? 0.f : w1;
             w2 = s[nt][2] == 0.f ? 0.f : w2;
@@ -851,7 +888,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           for (int r = 0; r < 2; ++r) {
             if (in == 0 && w % PW == 0) {
               kv_lds<PW>(vst + (w / PW * 2 + r) * 32 * F::PIECE + lane * F::PIECE, vw[r]);
-              if constexpr (MASKED) {
+              if (BITS == 8 && masked) {        // (any INT code is finite; an E4M3 one may be a NaN)
 #pragma unroll
                 for (int i = 0; i < PW; ++i) vw[r][i] &= keep[r];
               }
@@ -870,214 +907,218 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
             kv_mma(o[mt][nt], pv[0][2 * in], pv[0][2 * in + 1], pv[1][2 * in], pv[1][2 * in + 1], b[nt][0], b[nt][1]);
         }
       }
-    };
-
-    int done = 0;
-    for (; done < count; ++done) {
-      const int s = (turn0 + done) % STAGES;
-      if (!mbar_wait(&bars[s], ((turn0 + done) / STAGES) & 1, &abort_flag)) {
-        ok = false;
-        break;
-      }
-      const uint32_t st = smem_addr(ring + s * F::BLOCK);
-      const bool gone = any_absent && absent[s] != 0;
-      if (gone || done < plain0 || done >= plain1) process(std::true_type{}, st, blk0 + done, gone);
-      else process(std::false_type{}, st, blk0 + done, false);
       __syncwarp();
-      if (issued < count) issue(issued++);
-      if ((done & 15) == 15) centre();
+      if (issued < count) {
+        if ((issued & 31) == 0) look_up(issued);
+        issue(issued++);
+      }
+      if constexpr (A::VRAW) {
+        // the offsets and zeros are taken off the accumulators, often enough
+        // that the sums of offset codes do not grow much past their difference
+        if ((done & 15) == 15 || done + 1 == count) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[mt][0][i] -= zs[mt / (MT / NG)][i];
+#pragma unroll
+          for (int k = 0; k < NG; ++k) zs[k][0] = zs[k][1] = zs[k][2] = zs[k][3] = 0.f;
+        }
+      }
     }
     turn = turn0 + count;
-    centre();
-    if (!ok) {
-      // a copy did not arrive in time: say so and wait, with the same limit,
-      // for the copies still in flight; the run ends here
-      if (lane == 0) {
-        set_flag(g.status, TTQ_FLAG_TIMEOUT);
-        abort_flag = 1;
-        for (int i = done; i < issued; ++i) {
-          int never = 0;
-          mbar_wait(&bars[(turn0 + i) % STAGES], ((turn0 + i) / STAGES) & 1, &never);
-        }
-      }
-      __syncwarp();
-    }
 
-    // ---- the end of the segment, or of this run's part of it
-    const float back = 1.f / vf;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float v = l[nt][c];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        l[nt][c] = v;
-        if (!(seen >> (2 * nt + c) & 1u)) m[nt][c] = kKvFloor;
-      }
-    // the four channels of m tiles mt and mt + 1 that this lane holds of a row
-    auto channel = [&](int mt) { return 2 * mt / (F::G / 8) * F::G + gr * (F::G / 8) + 2 * mt % (F::G / 8); };
-    auto four = [&](int mt, int nt, int c) {
-      return make_float4(o[mt][nt][c] * back, o[mt][nt][c + 2] * back, o[mt + 1][nt][c] * back, o[mt + 1][nt][c + 2] * back);
-    };
-    if (count == seg.blocks && !together) {     // the whole segment
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int64_t at = row_y[8 * nt + 2 * tq + c];
-          if (at >= 0) {
-#pragma unroll
-            for (int mt = 0; mt < MT; mt += 2) kv_store_row<HD>(a, at, seg.h, channel(mt), four(mt, nt, c), l[nt][c]);
-          }
-        }
-      __syncwarp();                             // row_y is written again by the next segment
-      continue;
-    }
-
-    // a partial result: a run's in its first place if the segment began in
-    // an earlier run, else in its second; a thread block's in its first run's
-    // first
-    const int64_t end = x + left;               // the segment's last unit + 1
-    const KvParts parts(runs, end - seg.blocks - OV, end, OV, W);
-    auto slot_of = [&](int r) {
-      return a.part + (2 * static_cast<int64_t>(r) + (r == parts.first && !parts.merged(r) ? 1 : 0)) * A::SLOT;
-    };
-    const int mine = together ? static_cast<int>(blockIdx.x) * W : run;
-    float* slot = slot_of(mine);
-    if (together) {
-      __syncthreads();                          // every warp is done with its region
-      float* buf = reinterpret_cast<float*>(smem);
+    // ---- the end of the segment, or of this run's part of it: the warps'
+    // accumulators go to their regions, the rows' results from there to Y or,
+    // of a part, to the workspace
+    {
+      const float back = 1.f / vf;
+      float* tile = reinterpret_cast<float*>(ring);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int r = 8 * nt + 2 * tq + c;
+          float v = l[nt][c];
+          v += __shfl_xor_sync(0xffffffffu, v, 4);
+          v += __shfl_xor_sync(0xffffffffu, v, 8);
+          v += __shfl_xor_sync(0xffffffffu, v, 16);
           if (gr == 0) {
-            warp_m[warp][r] = m[nt][c];
-            warp_l[warp][r] = l[nt][c];
+            warp_l[warp][r] = v;
+            warp_m[warp][r] = (seen >> (2 * nt + c) & 1u) ? m[nt][c] : kKvFloor;
           }
 #pragma unroll
-          for (int mt = 0; mt < MT; mt += 2)
-            *reinterpret_cast<float4*>(buf + (warp * ROWS + r) * A::LDO + channel(mt)) = four(mt, nt, c);
+          for (int mt = 0; mt < MT; mt += 2) {
+            // the four channels of m tiles mt and mt + 1 that this lane holds of the row
+            const int ch = 2 * mt / (F::G / 8) * F::G + gr * (F::G / 8) + 2 * mt % (F::G / 8);
+            *reinterpret_cast<float4*>(tile + r * A::LDO + ch) =
+                make_float4(o[mt][nt][c] * back, o[mt][nt][c + 2] * back, o[mt + 1][nt][c] * back, o[mt + 1][nt][c + 2] * back);
+          }
         }
-      __syncthreads();
-      for (int i = tid; i < ROWS * (HD / 4); i += W * 32) {
+    }
+    const int width = together ? W * 32 : 32, me = together ? tid : lane;
+    auto sync = [&]() {
+      if (together) __syncthreads(); else __syncwarp();
+    };
+    sync();
+    const bool whole = count == seg.blocks && !together;
+    // a part's result: a run's in its first place if the segment began in an
+    // earlier run, else in its second; a thread block's in its first run's
+    // first
+    const int64_t end = x + left;               // the segment's last unit + 1
+    const KvParts parts(runs, whole ? 0 : end - seg.blocks - OV, whole ? 1 : end, whole ? 0 : OV, W);
+    auto place_of = [&](int r) { return 2 * r + (r == parts.first && !parts.merged(r) ? 1 : 0); };
+    const int mine = together ? static_cast<int>(blockIdx.x) * W : run;
+    auto store_row = [&](int r, int ch, float4 acc, float sum) {
+      const int rr = r0 + r, i_new = rr / a.per;
+      const int64_t row = static_cast<int64_t>(seg.row0 + i_new) * a.heads + seg.h * a.per + rr - i_new * a.per;
+      kv_store_row<HD>(a, row * HD, seg.h, ch, acc, sum);
+    };
+    {
+      const int w0 = together ? 0 : warp, w1 = together ? W : warp + 1;
+      float* slot = a.part + static_cast<int64_t>(place_of(mine)) * A::SLOT;
+#pragma unroll 1
+      for (int i = me; i < here * (HD / 4); i += width) {
         const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
-        if (r0 + r >= R) continue;
-        float mx = warp_m[0][r];
-#pragma unroll
-        for (int w = 1; w < W; ++w) mx = fmaxf(mx, warp_m[w][r]);
-        float sum = 0.f;
+        float mx = kKvFloor, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
+#pragma unroll 1
+        for (int w = w0; w < w1; ++w) mx = fmaxf(mx, warp_m[w][r]);
+#pragma unroll 1
+        for (int w = w0; w < w1; ++w) {
           const float f = kv_exp2(warp_m[w][r] - mx);
-          const float4 v = *reinterpret_cast<const float4*>(buf + (w * ROWS + r) * A::LDO + ch);
+          const float4 v = *reinterpret_cast<const float4*>(smem + w * A::WARP_BYTES + (r * A::LDO + ch) * 4);
           sum = fmaf(warp_l[w][r], f, sum);
           acc.x = fmaf(v.x, f, acc.x);
           acc.y = fmaf(v.y, f, acc.y);
           acc.z = fmaf(v.z, f, acc.z);
           acc.w = fmaf(v.w, f, acc.w);
         }
-        __stcg(reinterpret_cast<float4*>(slot + r * HD + ch), acc);
-        if (ch == 0) {
-          __stcg(slot + ROWS * HD + r, mx);
-          __stcg(slot + ROWS * (HD + 1) + r, sum);
+        if (whole) {
+          store_row(r, ch, acc, sum);
+        } else {
+          __stcg(reinterpret_cast<float4*>(slot + r * HD + ch), acc);
+          if (ch == 0) {
+            __stcg(slot + ROWS * HD + r, mx);
+            __stcg(slot + ROWS * (HD + 1) + r, sum);
+          }
         }
       }
-    } else {
+    }
+    if (!whole) {
+      // ---- tickets: the last of a group of results merges it, the last group
+      // the segment.  Groups of about the root of all results, where there are
+      // more than 8 (there are some 600 at most).
+      int group = parts.n;
+      if (parts.n > 8)
+        for (group = 8; group * group < parts.n;) ++group;
+      const int groups = (parts.n + group - 1) / group;
+      // the weights that a merge gives the results, in the region
+      int* place = reinterpret_cast<int*>(together ? smem : ring);
+      float* ms = reinterpret_cast<float*>(place + A::MOST);
+      float* ls = ms + A::MOST * ROWS;
+      float* sums = ls + A::MOST * ROWS;
+#pragma unroll 1
+      for (int level = groups > 1 ? 0 : 1; level < 2; ++level) {
+        // results k0, k0 + step, ...: n of them, their own or their groups'
+        const int k0 = level == 0 ? parts.index(mine) / group * group : 0;
+        const int step = level == 1 && groups > 1 ? group : 1;
+        const int n = level == 0 ? min(group, parts.n - k0) : step > 1 ? groups : parts.n;
+        sync();                                 // all of the result is written
+        // (a group of one may share its ticket with the next segment's first: it takes none)
+        if (level == 1 || n > 1) {
+          uint32_t* ticket = a.tickets + (level == 0 ? gridDim.x * W + parts.run(k0) : parts.first);
+          int last = 0;
+          if (me == 0) {
+            __threadfence();
+            last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(n - 1);
+            if (last) {
+              *ticket = 0;                      // left at zero
+              __threadfence();
+            }
+          }
+          if (together) {
+            if (tid == 0) last_flag = last;
+            __syncthreads();
+            last = last_flag;
+            __syncthreads();
+          } else {
+            last = __shfl_sync(0xffffffffu, last, 0);
+          }
+          if (!last) break;
+        }
+        for (int i = me; i < n; i += width) place[i] = place_of(parts.run(k0 + i * step));
+        sync();
+        const int mls = ROWS * (step > 1 ? HD + 2 : HD);
+        for (int i = me; i < n * ROWS; i += width) {
+          const float* p = a.part + static_cast<int64_t>(place[i / ROWS]) * A::SLOT + mls + i % ROWS;
+          ms[i] = __ldcg(p);
+          ls[i] = __ldcg(p + ROWS);
+        }
+        sync();
+        float* to = a.part + static_cast<int64_t>(place[0]) * A::SLOT;   // a group's result
+        if (me < here) {
+          float mx = kKvFloor, sum = 0.f;
+#pragma unroll 1
+          for (int i = 0; i < n; ++i) mx = fmaxf(mx, ms[i * ROWS + me]);
+#pragma unroll 1
+          for (int i = 0; i < n; ++i) {
+            const float f = kv_exp2(ms[i * ROWS + me] - mx);
+            ms[i * ROWS + me] = f;
+            sum = fmaf(ls[i * ROWS + me], f, sum);
+          }
+          sums[me] = sum;
+          if (level == 0) {
+            __stcg(to + ROWS * (HD + 2) + me, mx);
+            __stcg(to + ROWS * (HD + 3) + me, sum);
+          }
+        }
+        sync();
+        // 16 loads at a time that do not wait for one another
+#pragma unroll 1
+        for (int i0 = me; i0 < here * (HD / 4); i0 += 4 * width) {
+          float4 acc[4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int j0 = 0; j0 < n; j0 += 4) {
+            float4 v[4][4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int r = 8 * nt + 2 * tq + c;
-          if (r0 + r < R) {
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int mt = 0; mt < MT; mt += 2) __stcg(reinterpret_cast<float4*>(slot + r * HD + channel(mt)), four(mt, nt, c));
-            if (gr == 0) {
-              __stcg(slot + ROWS * HD + r, m[nt][c]);
-              __stcg(slot + ROWS * (HD + 1) + r, l[nt][c]);
+              for (int e = 0; e < 4; ++e) {
+                v[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int i = i0 + e * width;
+                if (j0 + j < n && i < here * (HD / 4))
+                  v[j][e] = kv_load_shared_result(a.part + static_cast<int64_t>(place[j0 + j]) * A::SLOT + i * 4);
+              }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int i = i0 + e * width;
+                const float f = j0 + j < n && i < here * (HD / 4) ? ms[(j0 + j) * ROWS + i / (HD / 4)] : 0.f;
+                acc[e].x = fmaf(v[j][e].x, f, acc[e].x);
+                acc[e].y = fmaf(v[j][e].y, f, acc[e].y);
+                acc[e].z = fmaf(v[j][e].z, f, acc[e].z);
+                acc[e].w = fmaf(v[j][e].w, f, acc[e].w);
+              }
+          }
+#pragma unroll 1
+          for (int e = 0; e < 4; ++e) {
+            const int i = i0 + e * width;
+            const float4 v = e == 0 ? acc[0] : e == 1 ? acc[1] : e == 2 ? acc[2] : acc[3];
+            if (i < here * (HD / 4)) {
+              if (level == 1) store_row(i / (HD / 4), (i % (HD / 4)) * 4, v, sums[i / (HD / 4)]);
+              else __stcg(reinterpret_cast<float4*>(to + i * 4), v);   // read by this thread alone
             }
           }
         }
-    }
-
-    // ---- tickets: the last of a group merges it, the last group the segment
-    const int width = together ? W * 32 : 32, me = together ? tid : lane;
-    // whether this was the last of n arrivals; the counter is left at zero
-    auto arrive = [&](uint32_t* counter, int n) -> bool {
-      if (together) __syncthreads(); else __syncwarp();   // all of the result is written
-      int last = 0;
-      if (me == 0) {
-        __threadfence();
-        last = atomicAdd(counter, 1u) == static_cast<uint32_t>(n - 1);
-        if (last) {
-          *counter = 0;
-          __threadfence();
-        }
       }
-      if (!together) return __shfl_sync(0xffffffffu, last, 0) != 0;
-      if (tid == 0) last_flag = last;
-      __syncthreads();
-      last = last_flag;
-      __syncthreads();
-      return last != 0;
-    };
-    // merges results k0, k0 + step, ... below k1: their own, or (step > 1)
-    // their groups'; into Y, or as a group into the place of the first
-    auto merge = [&](int k0, int k1, int step, bool whole) {
-      const int mls = ROWS * (step > 1 ? HD + 2 : HD);
-      for (int i = me; i < ROWS * (HD / 4); i += width) {
-        const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
-        if (r0 + r >= R) continue;
-        float mx = kKvFloor, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = k0; k < k1; k += step) {
-          const float* p = slot_of(parts.run(k));
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p + r * HD + ch));
-          const float mk = __ldcg(p + mls + r), lk = __ldcg(p + mls + ROWS + r);
-          const float m_new = fmaxf(mx, mk);
-          const float f = kv_exp2(mx - m_new), fk = kv_exp2(mk - m_new);
-          mx = m_new;
-          sum = fmaf(lk, fk, sum * f);
-          acc.x = fmaf(v.x, fk, acc.x * f);
-          acc.y = fmaf(v.y, fk, acc.y * f);
-          acc.z = fmaf(v.z, fk, acc.z * f);
-          acc.w = fmaf(v.w, fk, acc.w * f);
-        }
-        if (whole) {
-          const int rr = r0 + r, i_new = rr / a.per;
-          const int64_t row = static_cast<int64_t>(seg.row0 + i_new) * a.heads + seg.h * a.per + rr - i_new * a.per;
-          kv_store_row<HD>(a, row * HD, seg.h, ch, acc, sum);
-        } else {
-          float* p = slot_of(parts.run(k0));
-          __stcg(reinterpret_cast<float4*>(p + r * HD + ch), acc);   // read by this thread alone
-          if (ch == 0) {
-            __stcg(p + ROWS * (HD + 2) + r, mx);
-            __stcg(p + ROWS * (HD + 3) + r, sum);
-          }
-        }
-      }
-    };
-    constexpr int kGroup = 8;
-    int group = parts.n;                        // results of a group: about the root of all
-    if (parts.n > kGroup)
-      for (group = kGroup; group * group < parts.n;) ++group;
-    const int groups = (parts.n + group - 1) / group;
-    bool last = true;
-    if (groups > 1) {
-      const int k0 = parts.index(mine) / group * group, of = min(group, parts.n - k0);
-      // (a group of one may share its ticket with the next segment's first: it takes none)
-      if (of > 1) last = arrive(a.tickets + gridDim.x * W + parts.run(k0), of);
-      else if (together) __syncthreads();
-      else __syncwarp();
-      if (last) merge(k0, k0 + of, 1, false);
     }
-    if (last && arrive(a.tickets + parts.first, groups > 1 ? groups : parts.n))
-      merge(0, parts.n, groups > 1 ? group : 1, true);
+    if (!together) {
+      fence_proxy_async_smem();                 // the region is the copies' again
+      __syncwarp();
+    }
   }
 }
 
