@@ -14,8 +14,8 @@ constexpr size_t kStatusBytes = 4096;     // the least workspace an entry point 
 // at zero: the status word, then the attention's tickets from byte 256.
 constexpr size_t kKvHeader = 20480;
 constexpr size_t kKvTickets = 256;
-static_assert(kKvTickets + 2 * 4 * kKvPlanSMs * kKvAttentionWarps * sizeof(uint32_t) <= kKvHeader,
-              "two tickets a warp, of at most 4 blocks per SM");
+static_assert(kKvTickets + 2 * 4 * kKvPlanSMs * sizeof(uint32_t) <= kKvHeader,
+              "two tickets a block, of at most 4 blocks per SM");
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -101,7 +101,7 @@ KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows
                                : kv_attention_ctas_hd256(bits, group, p.nt);
   p.grid = ctas * kKvPlanSMs;
   p.slot_floats = static_cast<int64_t>(8 * p.nt) * (hd + 4);
-  p.part_bytes = static_cast<int64_t>(p.grid) * kKvAttentionWarps * 2 * p.slot_floats * 4;
+  p.part_bytes = static_cast<int64_t>(p.grid) * 2 * p.slot_floats * 4;
   return p;
 }
 

@@ -7,14 +7,17 @@
 // Work.  The rows of one key/value head (its query heads x the sequence's
 // new tokens) form tiles of 8 NT rows; a segment is one (sequence, head,
 // tile) with all blocks of 16 tokens that it may see.  All segments'
-// blocks, laid end to end, are cut into equal runs, one per warp of the
-// grid, so that contexts of any lengths load the SMs evenly and no warp
-// waits for another.  A warp whose run ends inside a segment leaves a partial
-// result (running maximum, sum and accumulator) in the workspace; the warp
-// whose ticket is the last of the segment's merges them in their order, so
-// that the result does not depend on who is last.  Where all warps of a
-// thread block work on one segment they merge theirs first, and where there
-// are many results groups of them are merged before the whole.
+// blocks, laid end to end, are cut into equal runs, one per thread block of
+// the grid, so that contexts of any lengths load the SMs evenly.  The warps
+// of a block share out its part of a segment, keep softmax states of their
+// own and merge them at its end.  Of a segment that several runs share each
+// leaves a partial result (running maximum, sum and accumulator) in the
+// workspace, and the one whose ticket is the segment's last merges them in
+// their order, so that the result does not depend on who is last; where
+// there are many, groups of them are merged before the whole.
+// (One run per warp, with no barrier between warps, was measured too: it
+// left every cut to a single warp's merge, 6 us at 2 to 9 results, and took
+// 97 us where this takes 88 for 64 contexts of up to 8192.)
 //
 // A warp brings its blocks through a ring of shared memory stages by bulk
 // copies, one per block (codes and pairs of K and V are contiguous).
@@ -63,8 +66,8 @@ struct KvAttention {
   static constexpr int ROWS = 8 * NT;               // query rows of a tile
   static constexpr int KS = HD / 16;                // k steps of the first product
   static constexpr int MT = HD / 16;                // m tiles of the second
-  static constexpr int QFRAG = NT * KS * 32 * 8;    // a warp's Q fragments
-  static constexpr int ROWINFO = ROWS * (16 + 8 * NG);   // and what it knows of its rows
+  static constexpr int QFRAG = NT * KS * 32 * 8;    // the tile's Q fragments
+  static constexpr int ROWINFO = ROWS * (16 + 8 * NG);   // and what is known of its rows
   static constexpr int LDO = HD + 4;                // padded row of the accumulators in shared memory
   static constexpr int TILE = ROWS * LDO * 4;       // their bytes
   // whether V's codes are taken raw and their zeros off the sums (see above)
@@ -75,27 +78,27 @@ struct KvAttention {
   // accumulators are at most 32 (128 registers), 3 for 64 (168), else 2; fewer
   // where their rings would not have two stages.
   static constexpr int SM_BYTES = 212 * 1024;
-  static constexpr int room(int ctas) { return SM_BYTES / (ctas * W) - QFRAG - ROWINFO - 512; }
+  static constexpr int room(int ctas) { return (SM_BYTES / ctas - QFRAG - ROWINFO - 2048) / W; }
+  static constexpr int fits(int ctas) { return room(ctas) >= 2 * F::BLOCK && room(ctas) >= TILE; }
   static constexpr int BY_REGS = HD * NT / 4 <= 32 ? 4 : HD * NT / 4 <= 64 ? 3 : 2;
-  static constexpr int CTAS = BY_REGS >= 4 && room(4) >= 2 * F::BLOCK ? 4 : BY_REGS >= 3 && room(3) >= 2 * F::BLOCK ? 3 : 2;
+  static constexpr int CTAS = BY_REGS >= 4 && fits(4) ? 4 : BY_REGS >= 3 && fits(3) ? 3 : 2;
   static constexpr int STAGES = room(CTAS) >= 4 * F::BLOCK ? 4 : 2;
-  static_assert(room(CTAS) >= 2 * F::BLOCK, "the ring needs two stages");
-  // a warp's region: ring, Q fragments, row information; at a segment's end
-  // its accumulators, then the weights of the results that it merges
-  static constexpr int REGION = STAGES * F::BLOCK + QFRAG + ROWINFO;
-  static constexpr int WARP_BYTES = REGION > TILE ? REGION : TILE;
+  static_assert(fits(CTAS), "the ring needs two stages, the accumulators their place");
+  // a warp's region: its ring; at a segment's end its accumulators
+  static constexpr int RING = STAGES * F::BLOCK;
+  static constexpr int WARP_BYTES = RING > TILE ? RING : TILE;
   static constexpr int MOST = 25;                   // results (or groups of results) merged at a time
-  static_assert((MOST * (2 * ROWS + 1) + ROWS) * 4 <= STAGES * F::BLOCK + QFRAG, "weights fit the region");
-  // dynamic shared memory: the warps' regions, then 16 bytes a sequence
-  static constexpr int SMEM = W * WARP_BYTES;
+  static_assert((MOST * (2 * ROWS + 1) + ROWS) * 4 <= W * WARP_BYTES, "their weights fit the regions");
+  // dynamic shared memory: the warps' regions, the tile's, 16 bytes a sequence
+  static constexpr int SMEM = W * WARP_BYTES + QFRAG + ROWINFO;
   // a partial result: accumulators, m and l, m and l of the group merged here
   static constexpr int SLOT = ROWS * (HD + 4);
   // what a segment costs besides its blocks, in blocks: its rows of Q, the
-  // first copy's latency and its end
-  static constexpr int OVERHEAD = 6;
+  // first copies' latency, the merge of the warps' results
+  static constexpr int OVERHEAD = 16;
   // the least a run has, so that short contexts are not cut into pieces
   // whose merge costs more than they do
-  static constexpr int LEAST = OVERHEAD + 4;
+  static constexpr int LEAST = OVERHEAD + 8;
 };
 
 __device__ __forceinline__ void kv_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -302,43 +305,6 @@ struct KvRuns {
   }
 };
 
-// The partial results of a segment that several runs share: runs `first` to
-// `last` have one each, but a thread block in [block0, block1), all of whose
-// runs are the segment's, has one in all, in its first run's place.
-struct KvParts {
-  int first, last, block0, block1, W, n;
-  __device__ __forceinline__ KvParts(const KvRuns& r, int64_t begin, int64_t end, int overhead, int warps) : W(warps) {
-    int lo = r.of(begin);
-    first = lo;
-    while (r.start(first + 1) <= begin + overhead) ++first;
-    last = r.of(end - 1);
-    if (r.start(lo) != begin) ++lo;                 // the first run wholly in the segment
-    const int hi = r.start(last + 1) == end ? last + 1 : last;
-    block0 = (lo + W - 1) / W;
-    block1 = hi / W;
-    if (block1 <= block0) {
-      block0 = block1 = 0;
-      n = last - first + 1;
-    } else {
-      n = block1 - block0 + max(block0 * W - first, 0) + last + 1 - block1 * W;
-    }
-  }
-  // the run that holds result k (0 <= k < n), and the result that run r holds
-  __device__ __forceinline__ int run(int k) const {
-    if (block1 == 0) return first + k;
-    const int before = max(block0 * W - first, 0);
-    if (k < before) return first + k;
-    k -= before;
-    return k < block1 - block0 ? (block0 + k) * W : block1 * W + k - (block1 - block0);
-  }
-  __device__ __forceinline__ int index(int r) const {
-    if (block1 == 0 || r < block0 * W) return r - first;
-    const int before = max(block0 * W - first, 0);
-    return r < block1 * W ? before + r / W - block0 : before + block1 - block0 + r - block1 * W;
-  }
-  __device__ __forceinline__ bool merged(int r) const { return r >= block0 * W && r < block1 * W; }
-};
-
 template <int HD, int BITS, int NG, int NT>
 __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAttention<HD, BITS, NG, NT>::CTAS)
     kv_attention_kernel(const KvAttentionArgs a) {
@@ -356,8 +322,8 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, tq = lane & 3;      // row group and quarter of the MMA fragments
   uint8_t* ring = smem + warp * A::WARP_BYTES;
-  uint32_t* qfrag = reinterpret_cast<uint32_t*>(ring + STAGES * F::BLOCK);
-  uint64_t* row_mask = reinterpret_cast<uint64_t*>(ring + STAGES * F::BLOCK + A::QFRAG);
+  uint32_t* qfrag = reinterpret_cast<uint32_t*>(smem + W * A::WARP_BYTES);
+  uint64_t* row_mask = reinterpret_cast<uint64_t*>(smem + W * A::WARP_BYTES + A::QFRAG);
   float* q_factor = reinterpret_cast<float*>(row_mask + ROWS);   // t = <row, (c - z) s> * q_factor
   int* row_pos = reinterpret_cast<int*>(q_factor + ROWS);
   float* q_sum = reinterpret_cast<float*>(row_pos + ROWS);       // [NG][ROWS] sums of a row's group
@@ -412,7 +378,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     }
     if (lane == 0) {
       const int64_t total = base * g.kv_heads, most = kv_div(total + A::LEAST - 1, A::LEAST);
-      const int all = static_cast<int>(gridDim.x) * W, runs = most < all ? static_cast<int>(most) : all;
+      const int runs = most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x);
       runs_s.total = total;
       runs_s.runs = runs;
       runs_s.each = runs > 0 ? kv_div(total, runs) : 0;
@@ -421,10 +387,10 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
   }
   __syncthreads();
   const KvRuns runs = runs_s;
-  if (static_cast<int>(blockIdx.x) * W >= runs.runs) return;
-  const int run = static_cast<int>(blockIdx.x) * W + warp;
-  int64_t x = run < runs.runs ? runs.start(run) : 0;
-  const int64_t x1 = run < runs.runs ? runs.start(run + 1) : 0;
+  const int run = blockIdx.x;
+  if (run >= runs.runs) return;
+  int64_t x = runs.start(run);
+  const int64_t x1 = runs.start(run + 1);
 
   // ---- the segment at x; a segment's blocks follow OV units of its own
   // cost, so a run that begins within those begins with its first block
@@ -439,7 +405,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     seg.blocks = ((seg.kv - 1) >> 4) + 1 - seg.first;
     tiles = tiles_of(seg.n);
   };
-  if (x < x1) {
+  {
     const int64_t per_head_x = kv_div(x, g.kv_heads);
     int lo = 0, hi = g.batch - 1;               // first b with end * kv_heads > x
     while (lo < hi) {
@@ -453,16 +419,10 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     seg.h = static_cast<int>(tile) / tiles;
     seg.tile = static_cast<int>(tile) - seg.h * tiles;
   }
-  // whether all runs of this thread block are one segment's: the block's
-  // units lie within the segment of this run (then of all its runs)
-  const bool together = (static_cast<int>(blockIdx.x) + 1) * W <= runs.runs &&
-                        runs.start(static_cast<int>(blockIdx.x) * W) >= x + left - seg.blocks - OV &&
-                        runs.start((static_cast<int>(blockIdx.x) + 1) * W) <= x + left;
 
   const KvMagic<BITS> magic;
   int turn = 0;                                 // blocks waited for so far: stage and parity of the ring
-  bool ok = true;
-  for (bool started = false; x < x1 && ok; started = true) {
+  for (bool started = false; x < x1; started = true) {
     if (started && left == 0) {                 // the next segment
       if (++seg.tile == tiles) {
         seg.tile = 0;
@@ -470,47 +430,48 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       }
       left = seg.blocks + OV;
     }
-    // blocks [from, from + count) of it are this run's; none if only a part
-    // of its overhead is
+    // blocks [from, from + part) of it are this run's; none if only some of
+    // its overhead is
     const int64_t take = x1 - x < left ? x1 - x : left;
     const int from = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks);
     x += take;
     left -= take;
-    const int count = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks) - from;
+    const int part = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks) - from;
+    if (part == 0) continue;
+    // of these this warp's: [blk0, blk0 + count)
+    const int mine0 = static_cast<int>(static_cast<int64_t>(part) * warp / W);
+    const int count = static_cast<int>(static_cast<int64_t>(part) * (warp + 1) / W) - mine0;
+    const int blk0 = seg.first + from + mine0;
     const int old = seg.kv - seg.n;             // positions before the new ones
     const int R = seg.n * a.per, r0 = seg.tile * ROWS;
-    // (a run of overhead alone leaves no result of its own; within a block
-    // whose warps merge theirs it goes on without blocks)
-    if (count == 0 && !together) continue;
 
-    // ---- the tile's rows: their loads from Q are on their way while the
-    // pages are looked up and the copies start
+    // ---- the tile's rows, 2 NT to a warp: their loads from Q are on their
+    // way while the pages are looked up and the copies start
     constexpr int E = HD / 32;                  // consecutive channels of a lane
+    constexpr int OWN = ROWS / W;               // rows that a warp prepares
     const int here = min(R - r0, ROWS);         // rows of the tile
-    int64_t q_at = 0;                           // row `lane` of the tile in Q
-    if (lane < ROWS) {
-      const int rr = min(r0 + lane, R - 1), i_new = rr / a.per, head = seg.h * a.per + rr - i_new * a.per;
-      const int64_t row = seg.row0 + i_new;
-      q_at = row * a.q_row + head * a.q_head;
-      uint64_t mask = a.tree != nullptr ? a.tree[row] : (2ull << i_new) - 1ull;
-      row_mask[lane] = mask;
-      row_pos[lane] = old + __popcll(mask & ~(1ull << i_new));
-    }
-    uint32_t raw[8][E] = {};                    // E words of float32, E / 2 of 16-bit elements
-    auto load_rows = [&](int nt) {
-      const bool wide = a.q_type == kRowF32;
+    const bool wide = a.q_type == kRowF32;
+    uint32_t raw[OWN][E] = {};                  // E words of float32, E / 2 of 16-bit elements
+    {
+      int64_t q_at = 0;                         // row OWN warp + lane of the tile in Q
+      if (lane < OWN) {
+        const int r = OWN * warp + lane, rr = min(r0 + r, R - 1), i_new = rr / a.per;
+        const int64_t row = seg.row0 + i_new;
+        q_at = row * a.q_row + (seg.h * a.per + rr - i_new * a.per) * a.q_head;
+        const uint64_t mask = a.tree != nullptr ? a.tree[row] : (2ull << i_new) - 1ull;
+        row_mask[r] = mask;
+        row_pos[r] = old + __popcll(mask & ~(1ull << i_new));
+      }
       const uint8_t* q = static_cast<const uint8_t*>(a.Q) + lane * (wide ? 4 * E : 2 * E);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t at = __shfl_sync(0xffffffffu, q_at, nt * 8 + k);   // (rows that are not there: the last one)
+      for (int k = 0; k < OWN; ++k) {
+        const int64_t at = __shfl_sync(0xffffffffu, q_at, k);   // (of rows that are not there: the last one)
         if (wide) kv_load_words<E>(q + at * 4, raw[k]);
         else kv_load_words<E / 2>(q + at * 2, raw[k]);
       }
-    };
-    load_rows(0);
+    }
 
     // ---- start the copies
-    const int blk0 = seg.first + from;          // this run's first block of the segment
     const uint8_t* src = nullptr;               // this lane's block 32 k + lane
     bool any_absent = false;
     const int turn0 = turn;
@@ -553,62 +514,57 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 #pragma unroll
       for (int e = 0; e < E; ++e) dk[e] = a.Dk != nullptr ? __ldg(a.Dk + seg.h * HD + lane * E + e) : 1.f;
       const float factor = a.scale * (a.cap > 0.f ? kv_rcp(a.cap) : kKvLog2e);
-#pragma unroll 1
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt > 0) load_rows(nt);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = nt * 8 + k;
-          float v[E], big = 0.f;
+      for (int k = 0; k < OWN; ++k) {
+        const int r = OWN * warp + k;
+        float v[E], big = 0.f;
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const uint32_t w = raw[k][e / 2];
-            const float bf = __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
-            const float hf = __half2float(e & 1 ? u32_as_h2(w).y : u32_as_h2(w).x);
-            const float x = a.q_type == kRowF32 ? __uint_as_float(raw[k][e]) : a.q_type == kRowBF16 ? bf : hf;
-            v[e] = r < here ? x * dk[e] : 0.f;
-            big = fmaxf(big, fabsf(v[e]));
-          }
-          // the row's largest magnitude: bits of non-negative floats order as integers
-          const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-          const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
-          const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^-(ex - 127)
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const int c = lane * E + e, kg = c / F::G, j = c % F::G;
-            const int quarter = j / (F::G / 4), idx = kg * (F::G / 4) + j % (F::G / 4);
-            qfrag[((nt * KS + idx / 4) * 32 + 4 * k + quarter) * 2 + (idx % 4) / 2] =
-                h2_as_u32(__floats2half2_rn(v[e] * down, v[e + 1] * down));
-          }
-          if (lane == 0)
-            q_factor[r] = factor * __uint_as_float(static_cast<uint32_t>(ex) << 23);
+        for (int e = 0; e < E; ++e) {
+          const uint32_t w = raw[k][e / 2];
+          const float bf = __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
+          const float hf = __half2float(e & 1 ? u32_as_h2(w).y : u32_as_h2(w).x);
+          const float q = wide ? __uint_as_float(raw[k][e]) : a.q_type == kRowBF16 ? bf : hf;
+          v[e] = r < here ? q * dk[e] : 0.f;
+          big = fmaxf(big, fabsf(v[e]));
         }
-      }
-      __syncwarp();
-      if constexpr (BITS != 8) {
-        // the sums of each group of the rounded rows: the first product with
-        // ones, and (INT2, whose fields' offsets differ) with the offsets, as codes
-#pragma unroll 1
-        for (int kn = 0; kn < NG * NT; ++kn) {
-          const int k = kn / NT, nt = kn % NT;
-          float one[4] = {}, off[4] = {};
+        // the row's largest magnitude: bits of non-negative floats order as integers
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+        const int ex = min(max(static_cast<int>(top >> 23), 1), 253);
+        const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^-(ex - 127)
 #pragma unroll
-          for (int j = 0; j < KS / NG; ++j) {
-            const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * KS + k * (KS / NG) + j) * 32 + lane) * 2);
-            kv_mma(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, bq.x, bq.y);
-            if constexpr (BITS == 2) kv_mma(off, A::EVEN, A::EVEN, A::ODD, A::ODD, bq.x, bq.y);
-          }
-          if (gr == 0) {
-            *reinterpret_cast<float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq) = make_float2(one[0], one[1]);
-            if constexpr (BITS == 2)
-              *reinterpret_cast<float2*>(q_off + k * ROWS + 8 * nt + 2 * tq) = make_float2(off[0], off[1]);
-          }
+        for (int e = 0; e < E; e += 2) {
+          const int c = lane * E + e, kg = c / F::G, j = c % F::G;
+          const int quarter = j / (F::G / 4), idx = kg * (F::G / 4) + j % (F::G / 4);
+          qfrag[(((r >> 3) * KS + idx / 4) * 32 + 4 * (r & 7) + quarter) * 2 + (idx % 4) / 2] =
+              h2_as_u32(__floats2half2_rn(v[e] * down, v[e + 1] * down));
         }
-        __syncwarp();
+        if (lane == 0) q_factor[r] = factor * __uint_as_float(static_cast<uint32_t>(ex) << 23);
       }
     }
+    __syncthreads();
+    if constexpr (BITS != 8) {
+      // the sums of each group of the rounded rows: the first product with
+      // ones, and (INT2, whose fields' offsets differ) with the offsets, as codes
+#pragma unroll 1
+      for (int kn = warp; kn < NG * NT; kn += W) {
+        const int k = kn / NT, nt = kn % NT;
+        float one[4] = {}, off[4] = {};
+#pragma unroll
+        for (int j = 0; j < KS / NG; ++j) {
+          const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * KS + k * (KS / NG) + j) * 32 + lane) * 2);
+          kv_mma(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, bq.x, bq.y);
+          if constexpr (BITS == 2) kv_mma(off, A::EVEN, A::EVEN, A::ODD, A::ODD, bq.x, bq.y);
+        }
+        if (gr == 0) {
+          *reinterpret_cast<float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq) = make_float2(one[0], one[1]);
+          if constexpr (BITS == 2)
+            *reinterpret_cast<float2*>(q_off + k * ROWS + 8 * nt + 2 * tq) = make_float2(off[0], off[1]);
+        }
+      }
+      __syncthreads();
+    }
 
-    // ---- the loop over this run's blocks
+    // ---- the loop over this warp's blocks
     float o[MT][NT][4] = {};
     float m[NT][2] = {}, l[NT][2] = {};
     constexpr uint32_t ALL = (1u << (2 * NT)) - 1;
@@ -631,8 +587,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       const int stage = (turn0 + done) % STAGES, blk = blk0 + done;
       if (!mbar_wait(&bars[stage], ((turn0 + done) / STAGES) & 1, &abort_flag)) {
         // a copy did not arrive in time: say so and wait, with the same limit,
-        // for the copies still in flight; the run ends here
-        ok = false;
+        // for the copies still in flight; the results are not right any more
         if (lane == 0) {
           set_flag(g.status, TTQ_FLAG_TIMEOUT);
           abort_flag = 1;
@@ -955,127 +910,109 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           }
         }
     }
-    const int width = together ? W * 32 : 32, me = together ? tid : lane;
-    auto sync = [&]() {
-      if (together) __syncthreads(); else __syncwarp();
-    };
-    sync();
-    const bool whole = count == seg.blocks && !together;
-    // a part's result: a run's in its first place if the segment began in an
-    // earlier run, else in its second; a thread block's in its first run's
-    // first
-    const int64_t end = x + left;               // the segment's last unit + 1
-    const KvParts parts(runs, whole ? 0 : end - seg.blocks - OV, whole ? 1 : end, whole ? 0 : OV, W);
-    auto place_of = [&](int r) { return 2 * r + (r == parts.first && !parts.merged(r) ? 1 : 0); };
-    const int mine = together ? static_cast<int>(blockIdx.x) * W : run;
+    __syncthreads();
+    const bool failed = *static_cast<volatile int*>(&abort_flag) != 0;
+    const bool whole = part == seg.blocks;
     auto store_row = [&](int r, int ch, float4 acc, float sum) {
       const int rr = r0 + r, i_new = rr / a.per;
       const int64_t row = static_cast<int64_t>(seg.row0 + i_new) * a.heads + seg.h * a.per + rr - i_new * a.per;
       kv_store_row<HD>(a, row * HD, seg.h, ch, acc, sum);
     };
-    {
-      const int w0 = together ? 0 : warp, w1 = together ? W : warp + 1;
-      float* slot = a.part + static_cast<int64_t>(place_of(mine)) * A::SLOT;
+    // a part's result is in the run's first place if the segment began in an
+    // earlier run, else in its second
+    float* slot = a.part + (2 * static_cast<int64_t>(run) + (from > 0 ? 0 : 1)) * A::SLOT;
 #pragma unroll 1
-      for (int i = me; i < here * (HD / 4); i += width) {
-        const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
-        float mx = kKvFloor, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int w = w0; w < w1; ++w) mx = fmaxf(mx, warp_m[w][r]);
-#pragma unroll 1
-        for (int w = w0; w < w1; ++w) {
-          const float f = kv_exp2(warp_m[w][r] - mx);
-          const float4 v = *reinterpret_cast<const float4*>(smem + w * A::WARP_BYTES + (r * A::LDO + ch) * 4);
-          sum = fmaf(warp_l[w][r], f, sum);
-          acc.x = fmaf(v.x, f, acc.x);
-          acc.y = fmaf(v.y, f, acc.y);
-          acc.z = fmaf(v.z, f, acc.z);
-          acc.w = fmaf(v.w, f, acc.w);
-        }
-        if (whole) {
-          store_row(r, ch, acc, sum);
-        } else {
-          __stcg(reinterpret_cast<float4*>(slot + r * HD + ch), acc);
-          if (ch == 0) {
-            __stcg(slot + ROWS * HD + r, mx);
-            __stcg(slot + ROWS * (HD + 1) + r, sum);
-          }
+    for (int i = tid; i < here * (HD / 4); i += W * 32) {
+      const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
+      float mx = warp_m[0][r], sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 1; w < W; ++w) mx = fmaxf(mx, warp_m[w][r]);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = kv_exp2(warp_m[w][r] - mx);
+        const float4 v = *reinterpret_cast<const float4*>(smem + w * A::WARP_BYTES + (r * A::LDO + ch) * 4);
+        sum = fmaf(warp_l[w][r], f, sum);
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      }
+      if (whole) {
+        store_row(r, ch, acc, sum);
+      } else {
+        __stcg(reinterpret_cast<float4*>(slot + r * HD + ch), acc);
+        if (ch == 0) {
+          __stcg(slot + ROWS * HD + r, mx);
+          __stcg(slot + ROWS * (HD + 1) + r, sum);
         }
       }
     }
     if (!whole) {
-      // ---- tickets: the last of a group of results merges it, the last group
-      // the segment.  Groups of about the root of all results, where there are
-      // more than 8 (there are some 600 at most).
-      int group = parts.n;
-      if (parts.n > 8)
-        for (group = 8; group * group < parts.n;) ++group;
-      const int groups = (parts.n + group - 1) / group;
-      // the weights that a merge gives the results, in the region
-      int* place = reinterpret_cast<int*>(together ? smem : ring);
-      float* ms = reinterpret_cast<float*>(place + A::MOST);
+      // ---- the segment's results are those of runs first to last.  Tickets:
+      // the last of a group of results merges it, the last group the segment.
+      // Groups of about the root of all results, where there are more than 12
+      // (there are some 600 at most).
+      const int64_t end = x + left, begin = end - seg.blocks;   // the units of its blocks
+      const int first = runs.of(begin), results = runs.of(end - 1) - first + 1;
+      auto place_of = [&](int k) { return 2 * (first + k) + (k == 0 ? 1 : 0); };
+      int group = results;
+      if (results > 12)
+        for (group = 4; group * group < results;) ++group;
+      const int groups = (results + group - 1) / group;
+      float* ms = reinterpret_cast<float*>(smem);     // weights that a merge gives the results
       float* ls = ms + A::MOST * ROWS;
       float* sums = ls + A::MOST * ROWS;
 #pragma unroll 1
       for (int level = groups > 1 ? 0 : 1; level < 2; ++level) {
         // results k0, k0 + step, ...: n of them, their own or their groups'
-        const int k0 = level == 0 ? parts.index(mine) / group * group : 0;
+        const int k0 = level == 0 ? (run - first) / group * group : 0;
         const int step = level == 1 && groups > 1 ? group : 1;
-        const int n = level == 0 ? min(group, parts.n - k0) : step > 1 ? groups : parts.n;
-        sync();                                 // all of the result is written
+        const int n = level == 0 ? min(group, results - k0) : step > 1 ? groups : results;
+        __syncthreads();                        // all of the result is written
         // (a group of one may share its ticket with the next segment's first: it takes none)
         if (level == 1 || n > 1) {
-          uint32_t* ticket = a.tickets + (level == 0 ? gridDim.x * W + parts.run(k0) : parts.first);
-          int last = 0;
-          if (me == 0) {
+          if (tid == 0) {
+            uint32_t* ticket = a.tickets + (level == 0 ? gridDim.x + first + k0 : first);
             __threadfence();
-            last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(n - 1);
+            const bool last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(n - 1);
             if (last) {
               *ticket = 0;                      // left at zero
               __threadfence();
             }
+            last_flag = last;
           }
-          if (together) {
-            if (tid == 0) last_flag = last;
-            __syncthreads();
-            last = last_flag;
-            __syncthreads();
-          } else {
-            last = __shfl_sync(0xffffffffu, last, 0);
-          }
-          if (!last) break;
+          __syncthreads();
+          if (!last_flag) break;
         }
-        for (int i = me; i < n; i += width) place[i] = place_of(parts.run(k0 + i * step));
-        sync();
         const int mls = ROWS * (step > 1 ? HD + 2 : HD);
-        for (int i = me; i < n * ROWS; i += width) {
-          const float* p = a.part + static_cast<int64_t>(place[i / ROWS]) * A::SLOT + mls + i % ROWS;
+        for (int i = tid; i < n * ROWS; i += W * 32) {
+          const float* p = a.part + static_cast<int64_t>(place_of(k0 + i / ROWS * step)) * A::SLOT + mls + i % ROWS;
           ms[i] = __ldcg(p);
           ls[i] = __ldcg(p + ROWS);
         }
-        sync();
-        float* to = a.part + static_cast<int64_t>(place[0]) * A::SLOT;   // a group's result
-        if (me < here) {
+        __syncthreads();
+        float* to = a.part + static_cast<int64_t>(place_of(k0)) * A::SLOT;   // a group's result
+        if (tid < here) {
           float mx = kKvFloor, sum = 0.f;
 #pragma unroll 1
-          for (int i = 0; i < n; ++i) mx = fmaxf(mx, ms[i * ROWS + me]);
+          for (int i = 0; i < n; ++i) mx = fmaxf(mx, ms[i * ROWS + tid]);
 #pragma unroll 1
           for (int i = 0; i < n; ++i) {
-            const float f = kv_exp2(ms[i * ROWS + me] - mx);
-            ms[i * ROWS + me] = f;
-            sum = fmaf(ls[i * ROWS + me], f, sum);
+            const float f = kv_exp2(ms[i * ROWS + tid] - mx);
+            ms[i * ROWS + tid] = f;
+            sum = fmaf(ls[i * ROWS + tid], f, sum);
           }
-          sums[me] = sum;
+          sums[tid] = sum;
           if (level == 0) {
-            __stcg(to + ROWS * (HD + 2) + me, mx);
-            __stcg(to + ROWS * (HD + 3) + me, sum);
+            __stcg(to + ROWS * (HD + 2) + tid, mx);
+            __stcg(to + ROWS * (HD + 3) + tid, sum);
           }
         }
-        sync();
+        __syncthreads();
         // 16 loads at a time that do not wait for one another
 #pragma unroll 1
-        for (int i0 = me; i0 < here * (HD / 4); i0 += 4 * width) {
+        for (int i0 = tid; i0 < here * (HD / 4); i0 += 4 * W * 32) {
           float4 acc[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1087,15 +1024,15 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 v[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                const int i = i0 + e * width;
+                const int i = i0 + e * W * 32;
                 if (j0 + j < n && i < here * (HD / 4))
-                  v[j][e] = kv_load_shared_result(a.part + static_cast<int64_t>(place[j0 + j]) * A::SLOT + i * 4);
+                  v[j][e] = kv_load_shared_result(a.part + static_cast<int64_t>(place_of(k0 + (j0 + j) * step)) * A::SLOT + i * 4);
               }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int i = i0 + e * width;
+                const int i = i0 + e * W * 32;
                 const float f = j0 + j < n && i < here * (HD / 4) ? ms[(j0 + j) * ROWS + i / (HD / 4)] : 0.f;
                 acc[e].x = fmaf(v[j][e].x, f, acc[e].x);
                 acc[e].y = fmaf(v[j][e].y, f, acc[e].y);
@@ -1105,7 +1042,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           }
 #pragma unroll 1
           for (int e = 0; e < 4; ++e) {
-            const int i = i0 + e * width;
+            const int i = i0 + e * W * 32;
             const float4 v = e == 0 ? acc[0] : e == 1 ? acc[1] : e == 2 ? acc[2] : acc[3];
             if (i < here * (HD / 4)) {
               if (level == 1) store_row(i / (HD / 4), (i % (HD / 4)) * 4, v, sums[i / (HD / 4)]);
@@ -1115,10 +1052,9 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         }
       }
     }
-    if (!together) {
-      fence_proxy_async_smem();                 // the region is the copies' again
-      __syncwarp();
-    }
+    if (failed) return;                         // (set before the barrier above: the same for all threads)
+    fence_proxy_async_smem();                   // the regions are the copies' again
+    __syncthreads();
   }
 }
 

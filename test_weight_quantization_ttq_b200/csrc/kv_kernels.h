@@ -72,8 +72,8 @@ struct KvAttentionArgs {
   // ceil(2^40 / page_blocks): n * page_magic >> 40 is n / page_blocks for n < 2^28
   // and page_blocks <= 4096 (the product is off by less than n 4096 < 2^40)
   uint64_t page_magic = 0;
-  float* part = nullptr;        // two partial results per warp of the grid
-  uint32_t* tickets = nullptr;  // two per warp of the grid, zero before and after
+  float* part = nullptr;        // two partial results per block of the grid
+  uint32_t* tickets = nullptr;  // two per block of the grid, zero before and after
 };
 // How a launch is laid out: 8 nt query rows per tile, `grid` blocks of
 // kKvAttentionWarps warps, the floats of one partial result, and the bytes
