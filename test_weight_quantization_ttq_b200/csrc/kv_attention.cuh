@@ -149,68 +149,6 @@ __device__ __forceinline__ void kv_lane_words(uint32_t part, int lane, int half,
     kv_lds<PIECE / 4>(part + (c * 2 + half) * 32 * PIECE + lane * PIECE, v + c * (PIECE / 4));
 }
 
-// The offsets + zero that the pairs of a word carry: o[i] for the i-th place.
-template <int BITS>
-struct KvZero {
-  static constexpr int N = BITS == 8 ? 1 : 8 / BITS;   // different places of a half word's byte
-  __half2 o[N];
-  __device__ __forceinline__ void set(uint32_t z) {    // two binary16 zeros
-    if constexpr (BITS == 4) {
-      o[0] = __hadd2(u32_as_h2(z), u32_as_h2(0x64006400u));   // 1024 + z
-      o[1] = __hadd2(u32_as_h2(z), u32_as_h2(0x54005400u));   // 64 + z
-    } else if constexpr (BITS == 2) {
-      o[0] = __hadd2(u32_as_h2(z), u32_as_h2(0x64006400u));   // 1024 + z
-      o[1] = __hadd2(u32_as_h2(z), u32_as_h2(0x5C005C00u));   // 256 + z
-      o[2] = __hadd2(u32_as_h2(z), u32_as_h2(0x54005400u));   // 64 + z
-      o[3] = __hadd2(u32_as_h2(z), u32_as_h2(0x4C004C00u));   // 16 + z
-    }
-  }
-};
-
-// (w & MASK) | magic in one instruction: a LOP3 takes one constant, so the
-// other has to be in a register (left to the compiler it became two; with
-// half of all instructions of the loop here, 149 of 474 per block were these).
-template <uint32_t MASK>
-__device__ __forceinline__ __half2 kv_field(uint32_t w, uint32_t magic) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(magic));
-  return u32_as_h2(r);
-}
-
-// The offsets under which the fields of a word's halves count as integers.
-template <int BITS>
-struct KvMagic {
-  uint32_t v[4];
-  __device__ __forceinline__ KvMagic() {
-    // kept opaque, so that they stay in registers
-    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(v[0]));
-    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(v[1]));
-    if constexpr (BITS == 2) {
-      asm volatile("mov.b32 %0, 0x5C005C00;" : "=r"(v[2]));
-      asm volatile("mov.b32 %0, 0x4C004C00;" : "=r"(v[3]));
-    }
-  }
-};
-
-// The pairs (c - z) of a word of INT codes: p[i] holds the i-th field of the
-// low and of the high half.
-template <int BITS>
-__device__ __forceinline__ void kv_int_pairs(uint32_t w, const KvZero<BITS>& z, const KvMagic<BITS>& c, uint32_t* p) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t u = i ? w >> 8 : w;
-    if constexpr (BITS == 4) {
-      p[2 * i] = h2_as_u32(__hsub2(kv_field<0x000F000Fu>(u, c.v[0]), z.o[0]));
-      p[2 * i + 1] = h2_as_u32(__hsub2(kv_field<0x00F000F0u>(u, c.v[1]), z.o[1]));
-    } else {
-      p[4 * i] = h2_as_u32(__hsub2(kv_field<0x00030003u>(u, c.v[0]), z.o[0]));
-      p[4 * i + 1] = h2_as_u32(__hsub2(kv_field<0x000C000Cu>(u, c.v[2]), z.o[1]));
-      p[4 * i + 2] = h2_as_u32(__hsub2(kv_field<0x00300030u>(u, c.v[1]), z.o[2]));
-      p[4 * i + 3] = h2_as_u32(__hsub2(kv_field<0x00C000C0u>(u, c.v[3]), z.o[3]));
-    }
-  }
-}
-
 // The offset pairs of a word: p[i] holds the i-th field of the low and of
 // the high half, plus 64 (even fields) or 64 / 16 (odd fields of INT4 / INT2).
 template <int BITS>

@@ -52,28 +52,6 @@ __device__ __forceinline__ bool kv_sequence(const KvGeometry& g, int b, KvSequen
          kv <= g.table_stride * g.page_blocks * 16;
 }
 
-// The sequence that holds row r, or -1: the last b with cu[b] <= r, when
-// r < cu[b + 1].
-__device__ __forceinline__ int kv_find_sequence(const KvGeometry& g, int64_t r) {
-  int lo = 0, hi = g.batch;          // cu[lo] <= r < cu[hi] once the ends are checked
-  if (g.batch == 0 || g.cu[0] > r || g.cu[g.batch] <= r) return -1;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (g.cu[mid] <= r) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
-// The block of position p of a sequence in the cache, for head h; null when
-// its page is not one of the cache's.
-__device__ __forceinline__ uint8_t* kv_block(const KvGeometry& g, int b, int p, int h, int block_bytes) {
-  const int blk = p >> 4;
-  const int page = g.table[b * g.table_stride + blk / g.page_blocks];
-  if (page < 0 || page >= g.num_pages) return nullptr;
-  return g.pages + page * g.page_bytes +
-         (static_cast<int64_t>(h) * g.page_blocks + blk % g.page_blocks) * block_bytes;
-}
-
 __device__ __forceinline__ uint32_t h2_as_u32(__half2 v) {
   uint32_t u;
   memcpy(&u, &v, 4);
@@ -95,6 +73,68 @@ __device__ __forceinline__ uint32_t kv_e4m3x2(uint32_t v) {
 __device__ __forceinline__ void kv_e4m3x4(uint32_t v, uint32_t& p0, uint32_t& p1) {
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
       "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}" : "=r"(p0), "=r"(p1) : "r"(v));
+}
+
+// (w & MASK) | magic in one instruction: a LOP3 takes one constant, so the
+// other has to be in a register (left to the compiler it becomes two).
+template <uint32_t MASK>
+__device__ __forceinline__ __half2 kv_field(uint32_t w, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(magic));
+  return u32_as_h2(r);
+}
+
+// The exponents under which the fields of a word's halves count as integers:
+// 1024, 64, 256 and 16 plus the code.
+template <int BITS>
+struct KvMagic {
+  uint32_t v[4];
+  __device__ __forceinline__ KvMagic() {
+    // kept opaque, so that they stay in registers
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(v[0]));
+    asm volatile("mov.b32 %0, 0x54005400;" : "=r"(v[1]));
+    if constexpr (BITS == 2) {
+      asm volatile("mov.b32 %0, 0x5C005C00;" : "=r"(v[2]));
+      asm volatile("mov.b32 %0, 0x4C004C00;" : "=r"(v[3]));
+    }
+  }
+};
+
+// The offsets + zero that the pairs of a word carry: o[i] for the i-th place.
+template <int BITS>
+struct KvZero {
+  static constexpr int N = BITS == 8 ? 1 : 8 / BITS;   // different places of a half word's byte
+  __half2 o[N];
+  __device__ __forceinline__ void set(uint32_t z) {    // two binary16 zeros
+    if constexpr (BITS == 4) {
+      o[0] = __hadd2(u32_as_h2(z), u32_as_h2(0x64006400u));   // 1024 + z
+      o[1] = __hadd2(u32_as_h2(z), u32_as_h2(0x54005400u));   // 64 + z
+    } else if constexpr (BITS == 2) {
+      o[0] = __hadd2(u32_as_h2(z), u32_as_h2(0x64006400u));   // 1024 + z
+      o[1] = __hadd2(u32_as_h2(z), u32_as_h2(0x5C005C00u));   // 256 + z
+      o[2] = __hadd2(u32_as_h2(z), u32_as_h2(0x54005400u));   // 64 + z
+      o[3] = __hadd2(u32_as_h2(z), u32_as_h2(0x4C004C00u));   // 16 + z
+    }
+  }
+};
+
+// The pairs (c - z) of a word of INT codes: p[i] holds the i-th field of the
+// low and of the high half; both steps are exact in binary16.
+template <int BITS>
+__device__ __forceinline__ void kv_int_pairs(uint32_t w, const KvZero<BITS>& z, const KvMagic<BITS>& c, uint32_t* p) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = i ? w >> 8 : w;
+    if constexpr (BITS == 4) {
+      p[2 * i] = h2_as_u32(__hsub2(kv_field<0x000F000Fu>(u, c.v[0]), z.o[0]));
+      p[2 * i + 1] = h2_as_u32(__hsub2(kv_field<0x00F000F0u>(u, c.v[1]), z.o[1]));
+    } else {
+      p[4 * i] = h2_as_u32(__hsub2(kv_field<0x00030003u>(u, c.v[0]), z.o[0]));
+      p[4 * i + 1] = h2_as_u32(__hsub2(kv_field<0x000C000Cu>(u, c.v[2]), z.o[1]));
+      p[4 * i + 2] = h2_as_u32(__hsub2(kv_field<0x00300030u>(u, c.v[1]), z.o[2]));
+      p[4 * i + 3] = h2_as_u32(__hsub2(kv_field<0x00C000C0u>(u, c.v[3]), z.o[3]));
+    }
+  }
 }
 
 // NaN-keeping minimum and maximum.

@@ -1,0 +1,140 @@
+// Writing rows of keys and values into the paged cache as group-wise codes,
+// and reading them back (ttq_kv_write, kv_write.cu; ttq_kv_read, kv_read.cu): what the
+// two share.
+//
+// The quantiser is the layer's own, in the same binary32 order (bit-exact
+// with ttq_quantize_weight_ex of the row as one row of a weight):
+//   x = k sqrt(D); m = min(0, min x); M = max(0, max x) over the group;
+//   s32 = (M - m) / (2^b - 1), at least 2^-14; s = binary16 round-up(s32);
+//   inv = 1 / s; z = clamp(rint(-m inv)); q = clamp(rint(x inv) + z),
+// rint of the exact product.  Symmetric and E4M3 codes likewise.
+//
+// Both kernels are bound by memory: a position of one head is 4 hd bytes of
+// bf16 rows against 2 (hd b / 8 + 4 hd / g) bytes of cache.  A warp takes the
+// K or the V part of one block (16 tokens of one head) and every lane the
+// codes that the layout gives it, so that codes move in 16-byte pieces with
+// all lanes contiguous, a group's range is found by 2 (K) or 3 (V) shuffles,
+// and a row's place is looked up once per 16 rows.  (A thread per 8 channels
+// of one row, with its own search, took 56 and 70 us where these take WW and
+// RR: for the prompts of 5 requests with INT4 codes, and 32785 positions.)
+// Rows of the dense tensors are read 16 bytes a lane; they are written
+// through shared memory, so that a store covers whole rows.
+#pragma once
+
+#include <type_traits>
+
+#include "kv_device.cuh"
+#include "ttq_kernels.h"
+
+namespace ttq {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+
+// The work of a call: for each sequence the blocks that its rows lie in.
+// seqs[b] = {end of its blocks in the sum over the sequences, kv, row0, n}.
+__device__ __forceinline__ int schedule(const KvGeometry& g, int4* seqs) {
+  __shared__ int total;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < g.batch; b0 += 32) {
+      const int b = b0 + lane;
+      KvSequence s = {};
+      int64_t v = 0;
+      if (b < g.batch) {
+        if (kv_sequence(g, b, s)) {
+          if (s.n > 0) v = ((s.kv - 1) >> 4) - ((s.kv - s.n) >> 4) + 1;
+        } else if (s.n != 0 && blockIdx.x == 0) {
+          set_flag(g.status, TTQ_FLAG_BAD_INDEX);
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (b < g.batch) seqs[b] = make_int4(static_cast<int>(base + v), s.kv, s.row0, s.n);
+      base += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) {
+      // rows that several sequences claim can add up to more blocks than there
+      // could be: then nothing is done
+      const bool fits = base <= 0x7FFFFFFF;
+      total = fits ? static_cast<int>(base) : 0;
+      if (!fits && blockIdx.x == 0) set_flag(g.status, TTQ_FLAG_BAD_INDEX);
+    }
+  }
+  __syncthreads();
+  return total;
+}
+
+// A warp's part of the work: the block of a sequence, and what of it is there.
+struct KvTask {
+  int which, h;        // K or V, head
+  uint8_t* part;       // its codes; null: the page is not one of the cache's
+  int row;             // row of the block's token 0 (may be below the sequence's first)
+  int lo, hi;          // tokens [lo, hi) of the block have rows
+};
+template <typename F>
+__device__ __forceinline__ KvTask task_of(const KvGeometry& g, const int4* seqs, int64_t t) {
+  KvTask k;
+  k.which = static_cast<int>(t & 1);
+  const int64_t u = t >> 1;
+  const int ordinal = static_cast<int>((u >> 32) == 0 ? static_cast<uint32_t>(u) / static_cast<uint32_t>(g.kv_heads)
+                                                      : u / g.kv_heads);
+  k.h = static_cast<int>(u - static_cast<int64_t>(ordinal) * g.kv_heads);
+  int lo = 0, hi = g.batch - 1;
+  while (lo < hi) {                     // first b with end > ordinal
+    const int mid = (lo + hi) >> 1;
+    if (seqs[mid].x > ordinal) hi = mid; else lo = mid + 1;
+  }
+  const int4 s = seqs[lo];
+  const int old = s.y - s.w, blk = (old >> 4) + ordinal - (lo > 0 ? seqs[lo - 1].x : 0);
+  k.lo = max(old - blk * 16, 0);
+  k.hi = min(s.y - blk * 16, 16);
+  k.row = s.z + blk * 16 - old;
+  const int page = g.table[lo * g.table_stride + blk / g.page_blocks];
+  k.part = nullptr;
+  if (page >= 0 && page < g.num_pages)
+    k.part = g.pages + page * g.page_bytes +
+             (static_cast<int64_t>(k.h) * g.page_blocks + blk % g.page_blocks) * F::BLOCK + k.which * F::V_OFFSET;
+  else if ((threadIdx.x & 31) == 0)
+    set_flag(g.status, TTQ_FLAG_BAD_INDEX);
+  return k;
+}
+
+// Calls f with the format's constants; false if it is not built.
+template <typename Fn>
+bool with_format(int hd, int bits, int group, Fn&& f) {
+  auto bits_of = [&](auto HDc, auto NGc) {
+    if (bits == 2) return f(HDc, std::integral_constant<int, 2>{}, NGc), true;
+    if (bits == 4) return f(HDc, std::integral_constant<int, 4>{}, NGc), true;
+    if (bits == 8) return f(HDc, std::integral_constant<int, 8>{}, NGc), true;
+    return false;
+  };
+  auto groups_of = [&](auto HDc) {
+    const int ng = hd / group;
+    if (ng == 1) return bits_of(HDc, std::integral_constant<int, 1>{});
+    if (ng == 2) return bits_of(HDc, std::integral_constant<int, 2>{});
+    if constexpr (decltype(HDc)::value >= 128)
+      if (ng == 4) return bits_of(HDc, std::integral_constant<int, 4>{});
+    return false;
+  };
+  if (hd == 64) return groups_of(std::integral_constant<int, 64>{});
+  if (hd == 128) return groups_of(std::integral_constant<int, 128>{});
+  if (hd == 256) return groups_of(std::integral_constant<int, 256>{});
+  return false;
+}
+
+// Thread blocks for the most parts of blocks that the rows may lie in, up to
+// `per_sm` a SM.
+unsigned part_grid(const KvGeometry& g, int num_sms, int per_sm) {
+  const int64_t blocks = (g.rows + 15) / 16 + 2 * static_cast<int64_t>(g.batch);
+  const int64_t need = (blocks * g.kv_heads * 2 + kWarps - 1) / kWarps, most = static_cast<int64_t>(num_sms) * per_sm;
+  return static_cast<unsigned>(need < most ? need : most);
+}
+
+}  // namespace
+}  // namespace ttq
