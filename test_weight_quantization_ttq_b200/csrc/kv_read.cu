@@ -27,7 +27,7 @@ __device__ __forceinline__ void load_code_words(const uint8_t* part, int lane, i
 __device__ __forceinline__ float2 floats_of(uint32_t p) { return __half22float2(u32_as_h2(p)); }
 
 template <int HD, int BITS, int NG, int TYPE>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a) {
+__global__ void __launch_bounds__(kThreads, HD == 256 || TYPE == kRowF32 ? 2 : 3) kv_read_kernel(const KvReadArgs a) {
   using F = KvFormat<HD, BITS, NG>;
   constexpr int G = F::G, WORDS = F::LB / 4, SIZE = TYPE == kRowF32 ? 4 : 2;
   constexpr int ROW = HD * SIZE + 16;            // padded row of a warp's tile
@@ -93,9 +93,10 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a) {
 #pragma unroll
               for (int e = e0; e < e0 + FW; e += 2) {
                 if (e < i * C || e >= (i + 1) * C) continue;   // (a word of two groups)
-                const float2 v = floats_of(p[(e - e0) / 2]);
-                x[e - i * C] = v.x * s;                        // exact: 8 bits at most times 11
-                x[e - i * C + 1] = v.y * s;
+                // exact: 8 bits at most times 11
+                const float2 v = __fmul2_rn(floats_of(p[(e - e0) / 2]), make_float2(s, s));
+                x[e - i * C] = v.x;
+                x[e - i * C + 1] = v.y;
               }
             }
             if (Dr != nullptr) {
@@ -122,9 +123,9 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a) {
 #pragma unroll
               for (int e = e0; e < e0 + U; ++e) {
                 if (e < i * C || e >= (i + 1) * C) continue;
-                const float2 v = floats_of(p[e - e0]);
-                x[e - i * C] = v.x * s0;
-                y[e - i * C] = v.y * s1;
+                const float2 v = __fmul2_rn(floats_of(p[e - e0]), make_float2(s0, s1));
+                x[e - i * C] = v.x;
+                y[e - i * C] = v.y;
               }
             }
             if (Dr != nullptr) {
@@ -142,15 +143,19 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a) {
     }
     __syncwarp();
     // the rows from the tile, 16 bytes a lane; of an absent page zeros
-    constexpr int LANES = HD * SIZE / 16;
+    constexpr int LANES = HD * SIZE / 16, STEP = LANES < 32 ? 32 / LANES : 1;   // tokens of a pass
+    const int64_t stride = static_cast<int64_t>(g.kv_heads) * HD * SIZE;
 #pragma unroll
-    for (int i = 0; i < 16 * LANES / 32; ++i) {
-      const int tok = (i * 32 + lane) / LANES, at = (i * 32 + lane) % LANES * 16;
-      if (tok < k.lo || tok >= k.hi) continue;
-      const uint4 v = k.part != nullptr ? *reinterpret_cast<const uint4*>(tile + tok * ROW + at) : make_uint4(0, 0, 0, 0);
-      uint8_t* y = static_cast<uint8_t*>(a.y[k.which]) +
-                   (static_cast<int64_t>(k.row + tok) * g.kv_heads + k.h) * HD * SIZE + at;
-      __stcs(reinterpret_cast<uint4*>(y), v);
+    for (int c = 0; c < (LANES > 32 ? LANES / 32 : 1); ++c) {
+      const int tok0 = lane / LANES, at = (c * 32 + lane) % LANES * 16;
+      const uint8_t* from = tile + tok0 * ROW + at;
+      uint8_t* y = static_cast<uint8_t*>(a.y[k.which]) + (k.row + tok0) * stride + k.h * HD * SIZE + at;
+#pragma unroll
+      for (int i = 0; i < 16; i += STEP) {
+        const uint4 v = k.part != nullptr ? *reinterpret_cast<const uint4*>(from + i * ROW) : make_uint4(0, 0, 0, 0);
+        if (tok0 + i >= k.lo && tok0 + i < k.hi) __stcs(reinterpret_cast<uint4*>(y), v);
+        y += STEP * stride;
+      }
     }
   }
 }
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a) {
 cudaError_t launch_kv_read(const KvReadArgs& a, int hd, int bits, int group, int dtype,
                            int num_sms, cudaStream_t stream) {
   cudaError_t e = cudaErrorInvalidValue;
-  const dim3 grid(part_grid(a.g, num_sms, 4));
+  const dim3 grid(part_grid(a.g, num_sms, hd == 256 || dtype == kRowF32 ? 2 : 3));
   with_format(hd, bits, group, [&](auto HDc, auto BITSc, auto NGc) {
     constexpr int HD = decltype(HDc)::value, BITS = decltype(BITSc)::value, NG = decltype(NGc)::value;
     auto* k = dtype == kRowF32    ? kv_read_kernel<HD, BITS, NG, kRowF32>

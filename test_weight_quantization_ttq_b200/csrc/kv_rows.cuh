@@ -129,11 +129,16 @@ bool with_format(int hd, int bits, int group, Fn&& f) {
 }
 
 // Thread blocks for the most parts of blocks that the rows may lie in, up to
-// `per_sm` a SM.
+// `per_sm` a SM (what is resident, so that all end together).  Where there
+// are more parts than warps the step of a warp, grid * kWarps parts, is made
+// a multiple of the heads' parts, so that a warp stays at its head.
 unsigned part_grid(const KvGeometry& g, int num_sms, int per_sm) {
   const int64_t blocks = (g.rows + 15) / 16 + 2 * static_cast<int64_t>(g.batch);
   const int64_t need = (blocks * g.kv_heads * 2 + kWarps - 1) / kWarps, most = static_cast<int64_t>(num_sms) * per_sm;
-  return static_cast<unsigned>(need < most ? need : most);
+  if (need <= most) return static_cast<unsigned>(need);
+  int64_t unit = g.kv_heads;                    // kv_heads / gcd(kv_heads, kWarps / 2)
+  for (int w = kWarps / 2; w > 1 && unit % 2 == 0; w /= 2) unit /= 2;
+  return static_cast<unsigned>(most >= unit ? most / unit * unit : most);
 }
 
 }  // namespace
