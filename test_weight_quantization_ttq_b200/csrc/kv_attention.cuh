@@ -1047,15 +1047,8 @@ cudaError_t kv_attention_launch(const KvAttentionArgs& a, int bits, int group, c
     using A = KvAttention<HD, BITS, NG, NT>;
     auto* kernel = kv_attention_kernel<HD, BITS, NG, NT>;
     const int smem = A::SMEM + 16 * a.g.batch;
-    static std::atomic<uint64_t> set{0};   // devices (a bit each) whose limit was raised
-    int dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (dev >= 64 || !(set.load(std::memory_order_relaxed) & bit)) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM + 16 * kKvMaxBatch);
-      if (e != cudaSuccess) return;
-      set.fetch_or(bit, std::memory_order_relaxed);
-    }
+    static std::atomic<uint64_t> set{0};
+    if ((e = kv_allow_smem(reinterpret_cast<const void*>(kernel), A::SMEM + 16 * kKvMaxBatch, set)) != cudaSuccess) return;
     e = launch_kernel(kernel, dim3(p.grid), dim3(A::W * 32), smem, stream, true, a);
   });
   return e;

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace ttq {
 
 constexpr int kKvMaxBatch = 1024;
@@ -22,6 +24,19 @@ constexpr int kv_code_bytes(int hd, int bits) { return 16 * hd * bits / 8; }
 constexpr int kv_pair_bytes(int hd, int group) { return 16 * (hd / group) * 4; }
 constexpr int kv_block_bytes(int hd, int bits, int group) {
   return 2 * (kv_code_bytes(hd, bits) + kv_pair_bytes(hd, group));
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device;
+// `set` remembers the devices (a bit each) that it was done for.
+inline cudaError_t kv_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (set.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // The cache and the batch as the kernels take them.

@@ -15,8 +15,8 @@ template <int BITS, bool SYM>
 __device__ __forceinline__ KvGroup group_of(float mn, float mx, uint32_t& flags) {
   constexpr int QMAX = (1 << BITS) - 1;
   KvGroup k;
-  const float range = __fsub_rn(mx, mn);
-  const float span = (BITS == 8 || SYM) ? kv_max_nan(mx, -mn) : range;
+  // the range; of the symmetric schemes the largest magnitude (mn is 0)
+  const float range = __fsub_rn(mx, mn), span = range;
   float s32;
   if constexpr (BITS == 8) s32 = div_by_const<448>(span);
   else s32 = div_by_const<SYM ? (1 << (BITS - 1)) - 1 : QMAX>(span);
@@ -62,19 +62,51 @@ __device__ __forceinline__ void scale_values(float2 (&x)[N], const float* h) {
     x[i + 1] = __fmul2_rn(x[i + 1], make_float2(f.z, f.w));
   }
 }
-template <int N, int LANES>
+template <bool ABS, int N, int LANES>
 __device__ __forceinline__ void range_of(const float2* x, float& mn, float& mx) {
-  mn = mx = 0.f;
+  mn = mx = 0.f;                                 // ABS: the largest magnitude alone, in mx
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    mn = min3_nan(mn, x[i].x, x[i].y);
-    mx = max3_nan(mx, x[i].x, x[i].y);
+    if constexpr (ABS) {
+      mx = max3_nan(mx, fabsf(x[i].x), fabsf(x[i].y));
+    } else {
+      mn = min3_nan(mn, x[i].x, x[i].y);
+      mx = max3_nan(mx, x[i].x, x[i].y);
+    }
   }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     if (!(LANES & o)) continue;
-    mn = kv_min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    if constexpr (!ABS) mn = kv_min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
     mx = kv_max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+}
+
+// The groups of N ranges that all of 2^k lanes know (lane number `me` among
+// them, LANES apart in the warp): each lane forms one (or N / 2^k), and they
+// tell each other.  store(n, pair) keeps the pair of group n.
+template <int BITS, bool SYM, int N, int COUNT, int APART, typename Store>
+__device__ __forceinline__ void share_groups(const float (&mn)[N], const float (&mx)[N], int me, KvGroup (&q)[N],
+                                             uint32_t& flags, Store&& store) {
+  const int lane = threadIdx.x & 31, first = lane - me * APART;
+#pragma unroll
+  for (int n0 = 0; n0 < N; n0 += COUNT) {
+    float a = mn[n0], b = mx[n0];
+#pragma unroll
+    for (int n = 1; n < COUNT && n0 + n < N; ++n)
+      if (me % (N < COUNT ? N : COUNT) == n) a = mn[n0 + n], b = mx[n0 + n];
+    const int own = n0 + me % (N < COUNT ? N : COUNT);
+    uint32_t f = 0;
+    const KvGroup k = group_of<BITS, SYM>(a, b, f);
+    if (me < N && store(own, k.pair)) flags |= f;
+#pragma unroll
+    for (int n = 0; n < COUNT && n0 + n < N; ++n) {
+      const int from = first + n * APART;
+      q[n0 + n].inv = __shfl_sync(0xffffffffu, k.inv, from);
+      const int zb = __shfl_sync(0xffffffffu, k.bad ? -1 : k.z, from);
+      q[n0 + n].bad = zb < 0;
+      q[n0 + n].z = max(zb, 0);
+    }
   }
 }
 
@@ -107,26 +139,25 @@ __device__ __forceinline__ void store_words(uint8_t* part, int lane, int half, c
     else *reinterpret_cast<uint4*>(p) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   }
 }
-// N pairs of consecutive values of a row.
+// N pairs of consecutive values of a row in shared memory.
 template <int TYPE, int N>
-__device__ __forceinline__ void load_values(const void* p, int64_t at, float2* x) {
+__device__ __forceinline__ void load_values(const uint8_t* p, float2* x) {
   if constexpr (TYPE == kRowF32) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + 2 * i));
+      const float4 v = reinterpret_cast<const float4*>(p)[i / 2];
       x[i] = make_float2(v.x, v.y);
       x[i + 1] = make_float2(v.z, v.w);
     }
   } else {
     uint32_t w[N];
-    const uint16_t* s = static_cast<const uint16_t*>(p) + at;
     if constexpr (N == 2) {
-      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(s));
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
       w[0] = v.x, w[1] = v.y;
     } else {
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(s + 2 * i));
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
         w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
       }
     }
@@ -137,30 +168,96 @@ __device__ __forceinline__ void load_values(const void* p, int64_t at, float2* x
   }
 }
 
+// A warp's shared memory: tiles of 16 rows (two up to 256 bytes a row: the
+// next part's rows are on their way while this one's are quantised; wider
+// rows would leave one block per SM, whose 8 warps one tile each hides less
+// than three blocks' do), and sqrt(D) of its head.
+template <int HD, int TYPE>
+struct WriteTile {
+  static constexpr int ROW_BYTES = HD * (TYPE == kRowF32 ? 4 : 2), ROW = ROW_BYTES + 16;   // padded
+  static constexpr int TILES = ROW_BYTES <= 256 ? 2 : 1;
+  static constexpr int TILE = 16 * ROW, WARP = TILES * TILE + HD * 4;
+  // thread blocks per SM by shared memory
+  static constexpr int CTAS = 222 * 1024 / (kWarps * WARP) >= 3 ? 3 : 222 * 1024 / (kWarps * WARP) >= 2 ? 2 : 1;
+};
+
 template <int HD, int BITS, int NG, bool SYM, int TYPE>
-__global__ void __launch_bounds__(kThreads, HD == 256 ? 2 : 3) kv_write_kernel(const KvWriteArgs a) {
+__global__ void __launch_bounds__(kThreads, WriteTile<HD, TYPE>::CTAS) kv_write_kernel(const KvWriteArgs a) {
   using F = KvFormat<HD, BITS, NG>;
+  using S = WriteTile<HD, TYPE>;
   constexpr int G = F::G, WORDS = F::LB / 4;
-  extern __shared__ int4 seqs[];
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t all_bars[2 * kWarps];
+  __shared__ int abort_flag;
   allow_dependents_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, tq = lane & 3;
+  uint64_t* bars = all_bars + 2 * warp;
+  if (lane == 0) {
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) abort_flag = 0;
   grid_dependency_wait();
   const KvGeometry& g = a.g;
-  const int lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
+  uint8_t* tiles = smem + warp * S::WARP;
+  int4* seqs = reinterpret_cast<int4*>(smem + kWarps * S::WARP);
   const int64_t total = static_cast<int64_t>(schedule(g, seqs)) * g.kv_heads * 2;
   // sqrt(D) of the head that this warp is at, as the lanes take it: a warp
   // keeps its head where the grid allows (see the launch)
-  float* h_tab = reinterpret_cast<float*>(seqs + g.batch) + (threadIdx.x >> 5) * HD;
+  float* h_tab = reinterpret_cast<float*>(tiles + S::TILES * S::TILE);
   int h_of = -1;
   uint32_t flags = 0;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < total;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const KvTask k = task_of<F>(g, seqs, t);
+  // the rows of a part into tile s: one bulk copy a row
+  auto fetch = [&](const KvTask& k, int s) {
+    const bool is = lane < 16 && lane >= k.lo && lane < k.hi && k.part != nullptr;
+    if (lane == 0) {
+      if (k.part != nullptr) mbar_arrive_expect_tx(&bars[s], (k.hi - k.lo) * S::ROW_BYTES);
+      else mbar_arrive(&bars[s]);
+    }
+    __syncwarp();                                // (the copies may not complete before they are expected)
+    if (is) {
+      const int64_t at = (k.row + lane) * a.row[k.which] + k.h * a.head[k.which];
+      bulk_load(smem_addr(tiles + s * S::TILE + lane * S::ROW),
+                static_cast<const uint8_t*>(a.x[k.which]) + at * (S::ROW_BYTES / HD), S::ROW_BYTES, &bars[s]);
+    }
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  KvTask next = {};
+  if (t < total) {
+    next = task_of<F>(g, seqs, t);
+    if (S::TILES == 2) fetch(next, 0);
+  }
+#pragma unroll 1
+  for (int turn = 0; t < total; t += step, ++turn) {
+    const KvTask k = next;
+    const int s = turn % S::TILES;
+    __syncwarp();                                // everyone is done with the tile that is filled next
+    if (S::TILES == 1) fetch(k, 0);
+    if (t + step < total) {
+      next = task_of<F>(g, seqs, t + step);
+      if (S::TILES == 2) fetch(next, (turn + 1) & 1);
+    }
+    if (!mbar_wait(&bars[s], (turn / S::TILES) & 1, &abort_flag)) {
+      // a copy did not arrive in time: say so, wait, with the same limit, for
+      // those in flight, and leave
+      if (lane == 0) {
+        set_flag(g.status, TTQ_FLAG_TIMEOUT);
+        abort_flag = 1;
+        int never = 0;
+        mbar_wait(&bars[s], (turn / S::TILES) & 1, &never);
+        if (S::TILES == 2 && t + step < total) mbar_wait(&bars[(turn + 1) & 1], ((turn + 1) >> 1) & 1, &never);
+      }
+      __syncwarp();
+      break;
+    }
     if (k.part == nullptr) continue;
+    const uint8_t* tile = tiles + s * S::TILE;
     const bool scaled = a.D[k.which] != nullptr;
     if (scaled && h_of != 2 * k.h + k.which) {
       h_of = 2 * k.h + k.which;
       const float* D = a.D[k.which] + k.h * HD;
-      __syncwarp();
 #pragma unroll
       for (int c = lane; c < HD; c += 32) {
         // K: the four quarters one after another, each with its part of all
@@ -170,113 +267,97 @@ __global__ void __launch_bounds__(kThreads, HD == 256 ? 2 : 3) kv_write_kernel(c
       }
       __syncwarp();
     }
-    const int64_t base = k.h * a.head[k.which];
+    // (tokens that have no row are quantised as what the tile holds there and not stored)
     if (k.which == 0) {
       // K: this lane's quarter of every group of tokens gr and gr + 8
       constexpr int C = G / 8;                   // pairs of a group
-      float2 x[2][NG * C];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int tok = gr + 8 * r;
-        if (tok >= k.lo && tok < k.hi) {
-          const int64_t at = (k.row + tok) * a.row[0] + base + tq * 2 * C;
-#pragma unroll
-          for (int i = 0; i < NG; ++i) load_values<TYPE, C>(a.x[0], at + i * G, x[r] + i * C);
-        } else {
-#pragma unroll
-          for (int j = 0; j < NG * C; ++j) x[r][j] = make_float2(0.f, 0.f);
-        }
-      }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int tok = gr + 8 * r;
         const bool is = tok >= k.lo && tok < k.hi;
-        if (scaled) scale_values(x[r], h_tab + tq * (HD / 4));
-        uint32_t w[WORDS] = {}, f = 0;
+        float2 x[NG * C];
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+          load_values<TYPE, C>(tile + tok * S::ROW + (i * G + tq * 2 * C) * (S::ROW_BYTES / HD), x + i * C);
+        if (scaled) scale_values(x, h_tab + tq * (HD / 4));
+        uint32_t w[WORDS] = {};
+        float mn[NG], mx[NG];
+#pragma unroll
+        for (int i = 0; i < NG; ++i) range_of<SYM || BITS == 8, C, 3>(x + i * C, mn[i], mx[i]);
+        KvGroup qs[NG];
+        share_groups<BITS, SYM, NG, 4, 1>(mn, mx, tq, qs, flags, [&](int n, uint32_t pair) {
+          if (is) *reinterpret_cast<uint32_t*>(k.part + F::CODES + (tok * NG + n) * 4) = pair;
+          return is;
+        });
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          float mn, mx;
-          range_of<C, 3>(x[r] + i * C, mn, mx);
-          const KvGroup q = group_of<BITS, SYM>(mn, mx, f);
-          if (is && tq == 0) *reinterpret_cast<uint32_t*>(k.part + F::CODES + (tok * NG + i) * 4) = q.pair;
-          const uint32_t z = static_cast<uint32_t>(q.z) * 0x00010001u;
+          const KvGroup q = qs[i];
+          [[maybe_unused]] const uint32_t z = static_cast<uint32_t>(q.z) * 0x00010001u;
           if (q.bad) {                           // codes of zero
 #pragma unroll
-            for (int j = 0; j < C; ++j) x[r][i * C + j] = make_float2(0.f, 0.f);
+            for (int j = 0; j < C; ++j) x[i * C + j] = make_float2(0.f, 0.f);
           }
 #pragma unroll
           for (int j = 0; j < C; ++j) {
             // a pair of channels is field j of a word's low and high half; E4M3: two bytes
             const int e = i * C + j;
             if constexpr (BITS == 8) {
-              w[e / 2] |= e4m3_codes(x[r][e], q.inv) << (e % 2 * 16);
+              w[e / 2] += e4m3_codes(x[e], q.inv) << (e % 2 * 16);
             } else {
               constexpr int FW = 16 / BITS;
-              const float2 n = rint_pair(x[r][e], q.inv);
-              w[e / FW] |= int_codes<BITS>(n.x, n.y, z) << (e % FW * BITS);
+              const float2 n = rint_pair(x[e], q.inv);
+              w[e / FW] += int_codes<BITS>(n.x, n.y, z) << (e % FW * BITS);
             }
           }
         }
-        if (is) {
-          store_words<F, WORDS>(k.part, lane, r, w);
-          flags |= f;
-        }
+        if (is) store_words<F, WORDS>(k.part, lane, r, w);
       }
     } else {
       // V: this lane's eighth of every group of tokens 2 tq, 2 tq + 1 (+ 8)
       constexpr int C = G / 16, U = 16 / BITS;   // pairs of a group; channels of a 16-bit unit
-      float2 x[2][2][NG * C];
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int tok = 2 * tq + p + 8 * r;
-          if (tok >= k.lo && tok < k.hi) {
-            const int64_t at = (k.row + tok) * a.row[1] + base + gr * 2 * C;
-#pragma unroll
-            for (int i = 0; i < NG; ++i) load_values<TYPE, C>(a.x[1], at + i * G, x[r][p] + i * C);
-          } else {
-#pragma unroll
-            for (int j = 0; j < NG * C; ++j) x[r][p][j] = make_float2(0.f, 0.f);
-          }
-        }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int tok = 2 * tq + 8 * r;
         const bool is[2] = {tok >= k.lo && tok < k.hi, tok + 1 >= k.lo && tok + 1 < k.hi};
         uint32_t w[WORDS] = {};
+        float2 x[2][NG * C];
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-          if (scaled) scale_values(x[r][p], h_tab + gr * (HD / 8));
+        for (int p = 0; p < 2; ++p) {
+#pragma unroll
+          for (int i = 0; i < NG; ++i)
+            load_values<TYPE, C>(tile + (tok + p) * S::ROW + (i * G + gr * 2 * C) * (S::ROW_BYTES / HD), x[p] + i * C);
+          if (scaled) scale_values(x[p], h_tab + gr * (HD / 8));
+        }
+        float mn[2 * NG], mx[2 * NG];            // of token p, group i at 2 i + p
+#pragma unroll
+        for (int n = 0; n < 2 * NG; ++n) range_of<SYM || BITS == 8, C, 28>(x[n % 2] + n / 2 * C, mn[n], mx[n]);
+        KvGroup qs[2 * NG];
+        share_groups<BITS, SYM, 2 * NG, 8, 4>(mn, mx, gr, qs, flags, [&](int n, uint32_t pair) {
+          const bool has = is[n % 2];
+          if (has) *reinterpret_cast<uint32_t*>(k.part + F::CODES + ((tok + n % 2) * NG + n / 2) * 4) = pair;
+          return has;
+        });
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          KvGroup q[2];
+          const KvGroup q[2] = {qs[2 * i], qs[2 * i + 1]};
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            float mn, mx;
-            uint32_t f = 0;
-            range_of<C, 28>(x[r][p] + i * C, mn, mx);
-            q[p] = group_of<BITS, SYM>(mn, mx, f);
+          for (int p = 0; p < 2; ++p)
             if (q[p].bad) {                      // codes of zero
 #pragma unroll
-              for (int j = 0; j < C; ++j) x[r][p][i * C + j] = make_float2(0.f, 0.f);
+              for (int j = 0; j < C; ++j) x[p][i * C + j] = make_float2(0.f, 0.f);
             }
-            if (is[p]) {
-              flags |= f;
-              if (gr == 0) *reinterpret_cast<uint32_t*>(k.part + F::CODES + ((tok + p) * NG + i) * 4) = q[p].pair;
-            }
-          }
-          const uint32_t z = static_cast<uint32_t>(q[0].z) | static_cast<uint32_t>(q[1].z) << 16;
+          [[maybe_unused]] const uint32_t z = static_cast<uint32_t>(q[0].z) | static_cast<uint32_t>(q[1].z) << 16;
 #pragma unroll
           for (int j = 0; j < C; ++j) {
             // both tokens' codes of a channel: the same field of the word's halves
             const int e = i * C + j;             // a pair of channels
             if constexpr (BITS == 8) {
-              w[e] = __byte_perm(e4m3_codes(x[r][0][e], q[0].inv), e4m3_codes(x[r][1][e], q[1].inv), 0x5410);
+              w[e] = __byte_perm(e4m3_codes(x[0][e], q[0].inv), e4m3_codes(x[1][e], q[1].inv), 0x5410);
             } else {
-              const float2 n0 = rint_pair(x[r][0][e], q[0].inv), n1 = rint_pair(x[r][1][e], q[1].inv);
+              const float2 n0 = rint_pair(x[0][e], q[0].inv), n1 = rint_pair(x[1][e], q[1].inv);
               const int f0 = 2 * e % U * BITS;
-              w[2 * e / U] |= int_codes<BITS>(n0.x, n1.x, z) << f0 | int_codes<BITS>(n0.y, n1.y, z) << (f0 + BITS);
+              w[2 * e / U] += int_codes<BITS>(n0.x, n1.x, z) << f0;
+              w[2 * e / U] += int_codes<BITS>(n0.y, n1.y, z) << (f0 + BITS);
             }
           }
         }
@@ -301,19 +382,27 @@ __global__ void __launch_bounds__(kThreads, HD == 256 ? 2 : 3) kv_write_kernel(c
 cudaError_t launch_kv_write(const KvWriteArgs& a, int hd, int bits, int group, bool symmetric,
                             int dtype, int num_sms, cudaStream_t stream) {
   cudaError_t e = cudaErrorInvalidValue;
-  const dim3 grid(part_grid(a.g, num_sms, hd == 256 ? 2 : 3));
   with_format(hd, bits, group, [&](auto HDc, auto BITSc, auto NGc) {
     constexpr int HD = decltype(HDc)::value, BITS = decltype(BITSc)::value, NG = decltype(NGc)::value;
-    auto go = [&](auto SYMc) {
+    auto go = [&](auto SYMc, auto TYPEc) {
       constexpr bool SYM = decltype(SYMc)::value;
-      auto* k = dtype == kRowF32    ? kv_write_kernel<HD, BITS, NG, SYM, kRowF32>
-                : dtype == kRowBF16 ? kv_write_kernel<HD, BITS, NG, SYM, kRowBF16>
-                                    : kv_write_kernel<HD, BITS, NG, SYM, kRowF16>;
-      e = launch_kernel(k, grid, dim3(kThreads), 16 * a.g.batch + kWarps * HD * 4, stream, true, a);
+      constexpr int TYPE = decltype(TYPEc)::value;
+      using S = WriteTile<HD, TYPE>;
+      constexpr int bytes = kWarps * S::WARP;
+      auto* k = kv_write_kernel<HD, BITS, NG, SYM, TYPE>;
+      static std::atomic<uint64_t> set{0};
+      if ((e = kv_allow_smem(reinterpret_cast<const void*>(k), bytes + 16 * kKvMaxBatch, set)) != cudaSuccess) return;
+      const dim3 grid(part_grid(a.g, num_sms, S::CTAS));
+      e = launch_kernel(k, grid, dim3(kThreads), bytes + 16 * a.g.batch, stream, true, a);
     };
-    if constexpr (BITS == 8) go(std::false_type{});
-    else if (symmetric) go(std::true_type{});
-    else go(std::false_type{});
+    auto of_type = [&](auto SYMc) {
+      if (dtype == kRowF32) go(SYMc, std::integral_constant<int, kRowF32>{});
+      else if (dtype == kRowBF16) go(SYMc, std::integral_constant<int, kRowBF16>{});
+      else go(SYMc, std::integral_constant<int, kRowF16>{});
+    };
+    if constexpr (BITS == 8) of_type(std::false_type{});
+    else if (symmetric) of_type(std::true_type{});
+    else of_type(std::false_type{});
   });
   return e;
 }
