@@ -67,6 +67,7 @@ ttq_status geometry(const ttq_kv_cache* c, const ttq_kv_batch* b, void* ws, size
   g->page_blocks = c->page_size / 16;
   g->kv_heads = c->kv_heads;
   g->table = b->page_table;
+  g->page_magic = ((1ull << 40) + g->page_blocks - 1) / g->page_blocks;
   g->table_stride = b->table_stride;
   g->kv_len = b->kv_len;
   g->cu = b->cu_new;
@@ -196,7 +197,6 @@ ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch
   a.window = window;
   a.tree = tree;
   a.Y = Y;
-  a.page_magic = ((1ull << 40) + a.g.page_blocks - 1) / a.g.page_blocks;
   a.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kKvTickets);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kKvHeader);
   return status_of(launch_kv_attention(a, cache->head_dim, cache->bits, cache->group, p,

@@ -149,6 +149,18 @@ __device__ __forceinline__ float kv_max_nan(float a, float b) {
   return r;
 }
 
+// 16 bytes global -> shared, asynchronously, past the L1 cache; zeros where
+// `there` is false (src is not read then).  Copies since the last commit form
+// a group; wait<N> returns when all but this thread's last N groups are done.
+__device__ __forceinline__ void kv_copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void kv_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void kv_copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // 8 consecutive elements of a row as float32, and back (rounded to nearest
 // even); all addresses are 16-byte aligned.
 template <int TYPE>

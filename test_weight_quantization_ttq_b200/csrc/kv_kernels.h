@@ -44,6 +44,9 @@ struct KvGeometry {
   uint8_t* pages = nullptr;
   int64_t num_pages = 0, page_bytes = 0;
   int page_blocks = 1;          // blocks of 16 tokens in a page
+  // ceil(2^40 / page_blocks): n * page_magic >> 40 is n / page_blocks for n < 2^28
+  // and page_blocks <= 4096 (the product is off by less than n 4096 < 2^40)
+  uint64_t page_magic = 0;
   int kv_heads = 1;
   const int32_t* table = nullptr;
   int64_t table_stride = 0;
@@ -84,9 +87,6 @@ struct KvAttentionArgs {
   int64_t window = 0;
   const uint64_t* tree = nullptr;
   void* Y = nullptr;
-  // ceil(2^40 / page_blocks): n * page_magic >> 40 is n / page_blocks for n < 2^28
-  // and page_blocks <= 4096 (the product is off by less than n 4096 < 2^40)
-  uint64_t page_magic = 0;
   float* part = nullptr;        // two partial results per block of the grid
   uint32_t* tickets = nullptr;  // two per block of the grid, zero before and after
 };

@@ -56,23 +56,29 @@ __global__ void __launch_bounds__(kThreads, HD == 256 || TYPE == kRowF32 ? 2 : 3
                        kv_pack2<TYPE>(x[i + 4], x[i + 5]), kv_pack2<TYPE>(x[i + 6], x[i + 7]));
     }
   };
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < total;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const KvTask k = task_of<F>(g, seqs, t);
+  KvWalk walk(g, total);
+  KvTask next = {};
+  if (walk.more()) next = walk.task(g, seqs);
+#pragma unroll 1
+  while (walk.more()) {
+    const KvTask k = next;
+    walk.next();
+    if (walk.more()) next = walk.task(g, seqs);
     if (a.y[k.which] == nullptr) continue;
+    const uint8_t* const part = part_of<F>(g, k);
     const float* Dr = a.Dr[k.which] != nullptr ? a.Dr[k.which] + k.h * HD : nullptr;
     __syncwarp();                                // the tile is free
-    if (k.part != nullptr) {
+    if (part != nullptr) {
       uint32_t w[2][WORDS], pair[2][2][NG];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        load_code_words<F, WORDS>(k.part, lane, r, w[r]);
+        load_code_words<F, WORDS>(part, lane, r, w[r]);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int i = 0; i < NG; ++i) {
             const int tok = k.which == 0 ? gr + 8 * r : 2 * tq + p + 8 * r;
-            pair[r][p][i] = *reinterpret_cast<const uint32_t*>(k.part + F::CODES + (tok * NG + i) * 4);
+            pair[r][p][i] = *reinterpret_cast<const uint32_t*>(part + F::CODES + (tok * NG + i) * 4);
           }
       }
       if (k.which == 0) {
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, HD == 256 || TYPE == kRowF32 ? 2 : 3
       uint8_t* y = static_cast<uint8_t*>(a.y[k.which]) + (k.row + tok0) * stride + k.h * HD * SIZE + at;
 #pragma unroll
       for (int i = 0; i < 16; i += STEP) {
-        const uint4 v = k.part != nullptr ? *reinterpret_cast<const uint4*>(from + i * ROW) : make_uint4(0, 0, 0, 0);
+        const uint4 v = part != nullptr ? *reinterpret_cast<const uint4*>(from + i * ROW) : make_uint4(0, 0, 0, 0);
         if (tok0 + i >= k.lo && tok0 + i < k.hi) __stcs(reinterpret_cast<uint4*>(y), v);
         y += STEP * stride;
       }

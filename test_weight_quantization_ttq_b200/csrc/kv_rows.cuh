@@ -15,8 +15,9 @@
 // codes that the layout gives it, so that codes move in 16-byte pieces with
 // all lanes contiguous, a group's range is found by 2 (K) or 3 (V) shuffles,
 // and a row's place is looked up once per 16 rows.  (A thread per 8 channels
-// of one row, with its own search, took 56 and 70 us where these take WW and
-// RR: for the prompts of 5 requests with INT4 codes, and 32785 positions.)
+// of one row, with its own search, took 84 and 70 us where these take 47 and
+// 36: the prompts of 5 requests, 6160 rows of 8 heads, written as INT4 codes
+// and read back, and 32785 positions read.)
 // Rows of the dense tensors are read 16 bytes a lane; they are written
 // through shared memory, so that a store covers whole rows.
 #pragma once
@@ -61,7 +62,7 @@ __device__ __forceinline__ int schedule(const KvGeometry& g, int4* seqs) {
     if (lane == 0) {
       // rows that several sequences claim can add up to more blocks than there
       // could be: then nothing is done
-      const bool fits = base <= 0x7FFFFFFF;
+      const bool fits = base <= 0x7F000000;
       total = fits ? static_cast<int>(base) : 0;
       if (!fits && blockIdx.x == 0) set_flag(g.status, TTQ_FLAG_BAD_INDEX);
     }
@@ -73,37 +74,68 @@ __device__ __forceinline__ int schedule(const KvGeometry& g, int4* seqs) {
 // A warp's part of the work: the block of a sequence, and what of it is there.
 struct KvTask {
   int which, h;        // K or V, head
-  uint8_t* part;       // its codes; null: the page is not one of the cache's
+  int page, at;        // the block's page as the table gives it, and its place among the page's
   int row;             // row of the block's token 0 (may be below the sequence's first)
   int lo, hi;          // tokens [lo, hi) of the block have rows
 };
+// The codes of a task; null: the page is not one of the cache's.  (Apart from
+// KvWalk::task, so that nothing waits for the table's entry before the task
+// is due.)
 template <typename F>
-__device__ __forceinline__ KvTask task_of(const KvGeometry& g, const int4* seqs, int64_t t) {
-  KvTask k;
-  k.which = static_cast<int>(t & 1);
-  const int64_t u = t >> 1;
-  const int ordinal = static_cast<int>((u >> 32) == 0 ? static_cast<uint32_t>(u) / static_cast<uint32_t>(g.kv_heads)
-                                                      : u / g.kv_heads);
-  k.h = static_cast<int>(u - static_cast<int64_t>(ordinal) * g.kv_heads);
-  int lo = 0, hi = g.batch - 1;
-  while (lo < hi) {                     // first b with end > ordinal
-    const int mid = (lo + hi) >> 1;
-    if (seqs[mid].x > ordinal) hi = mid; else lo = mid + 1;
-  }
-  const int4 s = seqs[lo];
-  const int old = s.y - s.w, blk = (old >> 4) + ordinal - (lo > 0 ? seqs[lo - 1].x : 0);
-  k.lo = max(old - blk * 16, 0);
-  k.hi = min(s.y - blk * 16, 16);
-  k.row = s.z + blk * 16 - old;
-  const int page = g.table[lo * g.table_stride + blk / g.page_blocks];
-  k.part = nullptr;
-  if (page >= 0 && page < g.num_pages)
-    k.part = g.pages + page * g.page_bytes +
-             (static_cast<int64_t>(k.h) * g.page_blocks + blk % g.page_blocks) * F::BLOCK + k.which * F::V_OFFSET;
-  else if ((threadIdx.x & 31) == 0)
-    set_flag(g.status, TTQ_FLAG_BAD_INDEX);
-  return k;
+__device__ __forceinline__ uint8_t* part_of(const KvGeometry& g, const KvTask& k) {
+  if (k.page >= 0 && k.page < g.num_pages)
+    return g.pages + k.page * g.page_bytes +
+           (static_cast<int64_t>(k.h) * g.page_blocks + k.at) * F::BLOCK + k.which * F::V_OFFSET;
+  if ((threadIdx.x & 31) == 0) set_flag(g.status, TTQ_FLAG_BAD_INDEX);
+  return nullptr;
 }
+// The parts that a warp takes, one after another: the sum over the sequences'
+// blocks, then the heads, then K and V.
+struct KvWalk {
+  int ordinal, rest;   // block and part of it
+  int step_ordinal, step_rest, parts;
+  int b = 0;           // sequence of the last task
+  int64_t left;        // parts of the call from here on
+  __device__ __forceinline__ KvWalk(const KvGeometry& g, int64_t total) {
+    parts = 2 * g.kv_heads;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const uint32_t step = gridDim.x * kWarps;    // (both below 2^32: the grid is what is resident)
+    ordinal = static_cast<uint32_t>(first) / parts;
+    rest = static_cast<uint32_t>(first) % parts;
+    step_ordinal = step / parts;
+    step_rest = step % parts;
+    left = total - first;
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next() {
+    left -= gridDim.x * kWarps;
+    ordinal += step_ordinal;
+    rest += step_rest;
+    if (rest >= parts) rest -= parts, ++ordinal;
+  }
+  __device__ __forceinline__ KvTask task(const KvGeometry& g, const int4* seqs) {
+    if (seqs[b].x <= ordinal) {
+      int lo = b + 1, hi = g.batch - 1;
+      while (lo < hi) {                 // first with end > ordinal
+        const int mid = (lo + hi) >> 1;
+        if (seqs[mid].x > ordinal) hi = mid; else lo = mid + 1;
+      }
+      b = lo;
+    }
+    const int4 s = seqs[b];
+    const int old = s.y - s.w, blk = (old >> 4) + ordinal - (b > 0 ? seqs[b - 1].x : 0);
+    const int pg = static_cast<int>(static_cast<uint64_t>(blk) * g.page_magic >> 40);   // blk / page_blocks
+    KvTask k;
+    k.page = __ldg(g.table + b * g.table_stride + pg);
+    k.at = blk - pg * g.page_blocks;
+    k.which = rest & 1;
+    k.h = rest >> 1;
+    k.lo = max(old - blk * 16, 0);
+    k.hi = min(s.y - blk * 16, 16);
+    k.row = s.z + blk * 16 - old;
+    return k;
+  }
+};
 
 // Calls f with the format's constants; false if it is not built.
 template <typename Fn>

@@ -187,17 +187,8 @@ __global__ void __launch_bounds__(kThreads, WriteTile<HD, TYPE>::CTAS) kv_write_
   using S = WriteTile<HD, TYPE>;
   constexpr int G = F::G, WORDS = F::LB / 4;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t all_bars[2 * kWarps];
-  __shared__ int abort_flag;
   allow_dependents_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, tq = lane & 3;
-  uint64_t* bars = all_bars + 2 * warp;
-  if (lane == 0) {
-    mbar_init(&bars[0], 1);
-    mbar_init(&bars[1], 1);
-    fence_barrier_init();
-  }
-  if (threadIdx.x == 0) abort_flag = 0;
   grid_dependency_wait();
   const KvGeometry& g = a.g;
   uint8_t* tiles = smem + warp * S::WARP;
@@ -208,51 +199,50 @@ __global__ void __launch_bounds__(kThreads, WriteTile<HD, TYPE>::CTAS) kv_write_
   float* h_tab = reinterpret_cast<float*>(tiles + S::TILES * S::TILE);
   int h_of = -1;
   uint32_t flags = 0;
-  // the rows of a part into tile s: one bulk copy a row
+  // the rows of a part into tile s; tokens that have none are zero.  (Bulk
+  // copies, one a row, were slower: each is issued for one lane at a time, and
+  // 16 of them took some 300 instructions of 1100.)
   auto fetch = [&](const KvTask& k, int s) {
-    const bool is = lane < 16 && lane >= k.lo && lane < k.hi && k.part != nullptr;
-    if (lane == 0) {
-      if (k.part != nullptr) mbar_arrive_expect_tx(&bars[s], (k.hi - k.lo) * S::ROW_BYTES);
-      else mbar_arrive(&bars[s]);
+    constexpr int LANES = S::ROW_BYTES / 16, STEP = LANES < 32 ? 32 / LANES : 1;   // tokens of a pass
+    const int64_t stride = a.row[k.which] * (S::ROW_BYTES / HD);
+    const uint32_t rows = (1u << k.hi) - (1u << k.lo);
+#pragma unroll
+    for (int c = 0; c < (LANES > 32 ? LANES / 32 : 1); ++c) {
+      const int tok0 = lane / LANES, at = (c * 32 + lane) % LANES * 16;
+      const uint32_t dst = smem_addr(tiles + s * S::TILE + tok0 * S::ROW + at);
+      const uint8_t* x = static_cast<const uint8_t*>(a.x[k.which]) + k.h * a.head[k.which] * (S::ROW_BYTES / HD) +
+                         (k.row + tok0) * stride + at;
+#pragma unroll
+      for (int i = 0; i < 16; i += STEP) {
+        kv_copy16(dst + i * S::ROW, x, rows >> (tok0 + i) & 1);
+        x += STEP * stride;
+      }
     }
-    __syncwarp();                                // (the copies may not complete before they are expected)
-    if (is) {
-      const int64_t at = (k.row + lane) * a.row[k.which] + k.h * a.head[k.which];
-      bulk_load(smem_addr(tiles + s * S::TILE + lane * S::ROW),
-                static_cast<const uint8_t*>(a.x[k.which]) + at * (S::ROW_BYTES / HD), S::ROW_BYTES, &bars[s]);
-    }
+    kv_copy_commit();
   };
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  KvWalk walk(g, total);
   KvTask next = {};
-  if (t < total) {
-    next = task_of<F>(g, seqs, t);
+  if (walk.more()) {
+    next = walk.task(g, seqs);
     if (S::TILES == 2) fetch(next, 0);
   }
 #pragma unroll 1
-  for (int turn = 0; t < total; t += step, ++turn) {
+  for (int turn = 0; walk.more(); ++turn) {
     const KvTask k = next;
     const int s = turn % S::TILES;
     __syncwarp();                                // everyone is done with the tile that is filled next
     if (S::TILES == 1) fetch(k, 0);
-    if (t + step < total) {
-      next = task_of<F>(g, seqs, t + step);
+    walk.next();
+    if (walk.more()) {
+      next = walk.task(g, seqs);
       if (S::TILES == 2) fetch(next, (turn + 1) & 1);
+    } else if (S::TILES == 2) {
+      kv_copy_commit();                          // (an empty group: one is always behind the one waited for)
     }
-    if (!mbar_wait(&bars[s], (turn / S::TILES) & 1, &abort_flag)) {
-      // a copy did not arrive in time: say so, wait, with the same limit, for
-      // those in flight, and leave
-      if (lane == 0) {
-        set_flag(g.status, TTQ_FLAG_TIMEOUT);
-        abort_flag = 1;
-        int never = 0;
-        mbar_wait(&bars[s], (turn / S::TILES) & 1, &never);
-        if (S::TILES == 2 && t + step < total) mbar_wait(&bars[(turn + 1) & 1], ((turn + 1) >> 1) & 1, &never);
-      }
-      __syncwarp();
-      break;
-    }
-    if (k.part == nullptr) continue;
+    kv_copy_wait<S::TILES - 1>();
+    __syncwarp();
+    uint8_t* const part = part_of<F>(g, k);
+    if (part == nullptr) continue;
     const uint8_t* tile = tiles + s * S::TILE;
     const bool scaled = a.D[k.which] != nullptr;
     if (scaled && h_of != 2 * k.h + k.which) {
@@ -267,7 +257,6 @@ __global__ void __launch_bounds__(kThreads, WriteTile<HD, TYPE>::CTAS) kv_write_
       }
       __syncwarp();
     }
-    // (tokens that have no row are quantised as what the tile holds there and not stored)
     if (k.which == 0) {
       // K: this lane's quarter of every group of tokens gr and gr + 8
       constexpr int C = G / 8;                   // pairs of a group
@@ -286,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, WriteTile<HD, TYPE>::CTAS) kv_write_
         for (int i = 0; i < NG; ++i) range_of<SYM || BITS == 8, C, 3>(x + i * C, mn[i], mx[i]);
         KvGroup qs[NG];
         share_groups<BITS, SYM, NG, 4, 1>(mn, mx, tq, qs, flags, [&](int n, uint32_t pair) {
-          if (is) *reinterpret_cast<uint32_t*>(k.part + F::CODES + (tok * NG + n) * 4) = pair;
+          if (is) *reinterpret_cast<uint32_t*>(part + F::CODES + (tok * NG + n) * 4) = pair;
           return is;
         });
 #pragma unroll
@@ -310,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, WriteTile<HD, TYPE>::CTAS) kv_write_
             }
           }
         }
-        if (is) store_words<F, WORDS>(k.part, lane, r, w);
+        if (is) store_words<F, WORDS>(part, lane, r, w);
       }
     } else {
       // V: this lane's eighth of every group of tokens 2 tq, 2 tq + 1 (+ 8)
@@ -334,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, WriteTile<HD, TYPE>::CTAS) kv_write_
         KvGroup qs[2 * NG];
         share_groups<BITS, SYM, 2 * NG, 8, 4>(mn, mx, gr, qs, flags, [&](int n, uint32_t pair) {
           const bool has = is[n % 2];
-          if (has) *reinterpret_cast<uint32_t*>(k.part + F::CODES + ((tok + n % 2) * NG + n / 2) * 4) = pair;
+          if (has) *reinterpret_cast<uint32_t*>(part + F::CODES + ((tok + n % 2) * NG + n / 2) * 4) = pair;
           return has;
         });
 #pragma unroll
@@ -362,13 +351,13 @@ __global__ void __launch_bounds__(kThreads, WriteTile<HD, TYPE>::CTAS) kv_write_
           }
         }
         if (is[0] && is[1]) {
-          store_words<F, WORDS>(k.part, lane, r, w);
+          store_words<F, WORDS>(part, lane, r, w);
         } else if (is[0] || is[1]) {
           // one token of the pair: its halves of the words, the other's stay
           const int p = is[1];
 #pragma unroll
           for (int i = 0; i < WORDS; ++i)
-            *reinterpret_cast<uint16_t*>(k.part + F::place(lane, r, i * 4 + 2 * p)) =
+            *reinterpret_cast<uint16_t*>(part + F::place(lane, r, i * 4 + 2 * p)) =
                 static_cast<uint16_t>(p ? w[i] >> 16 : w[i]);
         }
       }
