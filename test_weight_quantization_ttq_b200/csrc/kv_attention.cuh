@@ -95,7 +95,7 @@ struct KvAttention {
   static constexpr int SLOT = ROWS * (HD + 4);
   // what a segment costs besides its blocks, in blocks: its rows of Q, the
   // first copies' latency, the merge of the warps' results
-  static constexpr int OVERHEAD = 16;
+  static constexpr int OVERHEAD = NT == 1 ? 16 : 32;
   // the least a run has, so that short contexts are not cut into pieces
   // whose merge costs more than they do
   static constexpr int LEAST = OVERHEAD + 8;
@@ -126,6 +126,12 @@ __device__ __forceinline__ float kv_rcp(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// w = 0 where p = 0.  (Left to the compiler, what few blocks need becomes a
+// select for all of them.)
+__device__ __forceinline__ void kv_zero_with(float& w, float p) {
+  asm volatile("{\n\t.reg .pred z;\n\tsetp.eq.f32 z, %1, 0f00000000;\n\t@z mov.f32 %0, 0f00000000;\n\t}" : "+f"(w) : "f"(p));
 }
 
 // v read from shared memory as N words.
@@ -473,7 +479,8 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         for (int e = 0; e < E; e += 2) {
           const int c = lane * E + e, kg = c / F::G, j = c % F::G;
           const int quarter = j / (F::G / 4), idx = kg * (F::G / 4) + j % (F::G / 4);
-          qfrag[(((r >> 3) * KS + idx / 4) * 32 + 4 * (r & 7) + quarter) * 2 + (idx % 4) / 2] =
+          // two k steps of a lane stand side by side
+          qfrag[(((r >> 3) * (KS / 2) + idx / 8) * 32 + 4 * (r & 7) + quarter) * 4 + (idx % 8) / 2] =
               h2_as_u32(__floats2half2_rn(v[e] * down, v[e + 1] * down));
         }
         if (lane == 0) q_factor[r] = factor * __uint_as_float(static_cast<uint32_t>(ex) << 23);
@@ -489,7 +496,8 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         float one[4] = {}, off[4] = {};
 #pragma unroll
         for (int j = 0; j < KS / NG; ++j) {
-          const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * KS + k * (KS / NG) + j) * 32 + lane) * 2);
+          const int ks = k * (KS / NG) + j;
+          const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * (KS / 2) + ks / 2) * 32 + lane) * 4 + ks % 2 * 2);
           kv_mma(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, bq.x, bq.y);
           if constexpr (BITS == 2) kv_mma(off, A::EVEN, A::EVEN, A::ODD, A::ODD, bq.x, bq.y);
         }
@@ -519,6 +527,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       plain0 = need <= 0 ? 0 : need >= count ? count : static_cast<int>(need);
     }
     const int plain1 = (old >> 4) - blk0;                             // blocks before the new tokens
+    const uint32_t q_frags = smem_addr(qfrag) + lane * 16;
 
 #pragma unroll 1
     for (int done = 0; done < count; ++done) {
@@ -552,6 +561,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
         float acc[NT][4];
+        uint32_t bq[NT][4];                     // Q's fragments of two k steps
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 #pragma unroll
@@ -568,8 +578,9 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * KS + ks) * 32 + lane) * 2);
-            kv_mma(acc[nt], pa[0][2 * in], pa[1][2 * in], pa[0][2 * in + 1], pa[1][2 * in + 1], bq.x, bq.y);
+            if (ks % 2 == 0) kv_lds<4>(q_frags + (nt * (KS / 2) + ks / 2) * 512, bq[nt]);
+            kv_mma(acc[nt], pa[0][2 * in], pa[1][2 * in], pa[0][2 * in + 1], pa[1][2 * in + 1], bq[nt][ks % 2 * 2],
+                   bq[nt][ks % 2 * 2 + 1]);
           }
         }
         const float2 p0 = __half22float2(u32_as_h2(kp[0][k])), p1 = __half22float2(u32_as_h2(kp[1][k]));
@@ -675,20 +686,14 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           }
         }
       }
-      bool higher = !all_seen;                  // a scale or a score is well above the running ones
+      float top = 0.f, most = s[0][0];          // the largest scale and score (NaN aside)
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int k = 0; k < NG; ++k) top = fmaxf(top, fmaxf(vs[0][k], vs[1][k]));
 #pragma unroll
-        for (int k = 0; k < NG; ++k) higher |= vs[r][k] * vf > 64.f;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) higher |= s[nt][i] > kKvSlack;
-      // -- the running maxima move only then (and to a column's first score)
-      if (__any_sync(0xffffffffu, higher)) {
-        float top = 0.f;                        // the largest scale (NaN aside)
-#pragma unroll
-        for (int k = 0; k < NG; ++k) top = fmaxf(top, fmaxf(vs[0][k], vs[1][k]));
+      for (int i = 1; i < 4 * NT; ++i) most = fmaxf(most, s[i / 4][i % 4]);
+      // -- the running maxima move only when one is well above them (and to a
+      // column's first score)
+      if (__any_sync(0xffffffffu, !all_seen || top * vf > 64.f || most > kKvSlack)) {
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
         float fv = 1.f;
         if (top * vf > 64.f) {
@@ -750,10 +755,10 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         for (int nt = 0; nt < NT; ++nt) {
           float w0 = s[nt][0] * s0, w1 = s[nt][1] * s0, w2 = s[nt][2] * s1, w3 = s[nt][3] * s1;
           if (masked) {                         // a NaN scale reaches only those that see its token
-            w0 = s[nt][0] == 0.f ? 0.f : w0;
-            w1 = s[nt][1] == 0.f ? 0.f : w1;
-            w2 = s[nt][2] == 0.f ? 0.f : w2;
-            w3 = s[nt][3] == 0.f ? 0.f : w3;
+            kv_zero_with(w0, s[nt][0]);
+            kv_zero_with(w1, s[nt][1]);
+            kv_zero_with(w2, s[nt][2]);
+            kv_zero_with(w3, s[nt][3]);
           }
           b[nt][0] = kv_transpose(h2_as_u32(__floats2half2_rn(w0, w1)));
           b[nt][1] = kv_transpose(h2_as_u32(__floats2half2_rn(w2, w3)));

@@ -664,26 +664,27 @@ def _ints(t: torch.Tensor, name: str, shape) -> None:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}")
 
 
-def _rows_of(t: torch.Tensor, name: str, rows: int, heads, head_dim: int) -> None:
-    """t is [rows][heads][head_dim] with contiguous channels (heads None: any number)."""
+def _rows_of(t: torch.Tensor, name: str, rows: int, heads, head_dim: int) -> tuple:
+    """The strides of t, which is [rows][heads][head_dim] with contiguous channels (heads None: any number)."""
     if t.dtype not in _ROW_TYPES:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {list(_ROW_TYPES)}")
-    shape = t.shape
+    shape, strides = t.shape, t.stride()
     if len(shape) != 3 or shape[0] != rows or shape[2] != head_dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} has shape {tuple(shape)}, expected {(rows, '*' if heads is None else heads, head_dim)}")
-    if t.stride(2) != 1:
-        raise ValueError(f"the channels of {name} must be contiguous, got strides {t.stride()}")
+    if strides[2] != 1:
+        raise ValueError(f"the channels of {name} must be contiguous, got strides {strides}")
+    return strides
 
 
-def _strided(t: torch.Tensor, name: str, device: int) -> tuple:
+def _strided(t: torch.Tensor, name: str, rows: int, heads: int, strides: tuple, device: int) -> tuple:
     """(pointer, row stride, head stride) of a row tensor on this device."""
     if t.get_device() != device:
         raise ValueError(f"{name} must be a CUDA tensor on cuda:{device}, got {t.device}")
-    (rows, heads, _), (row, head, _), at = t.shape, t.stride(), t.data_ptr()
+    at = t.data_ptr()
     # the stride of a size that is not walked along says nothing
-    row, head = row if rows > 1 else 0, head if heads > 1 else 0
+    row, head = strides[0] if rows > 1 else 0, strides[1] if heads > 1 else 0
     if row % 8 or head % 8 or at % 16:
-        raise ValueError(f"the rows of {name} must be 16-byte aligned: strides {t.stride()} are not multiples of 8 "
+        raise ValueError(f"the rows of {name} must be 16-byte aligned: strides {strides} are not multiples of 8 "
                          "elements, or its first element is not at a 16-byte boundary")
     return at, row, head
 
@@ -705,6 +706,13 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_rows(rows, heads, head_dim, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised row tensor of the stream that the call runs on."""
+    if stream is None:    # with strides: 1 us less of host time
+        return torch.empty_strided((rows, heads, head_dim), (heads * head_dim, head_dim, 1), dtype=dtype, device=device)
+    return _empty((rows, heads, head_dim), dtype, device, stream)
 
 
 class KVCache:
@@ -803,16 +811,18 @@ def new_kv_workspace(cache, batch, heads=None, stream=None) -> torch.Tensor:
 def ttq_kv_write(cache, batch, K, V, ws=None, stream=None) -> None:
     """Quantises the rows of K and V [rows][kv_heads][head_dim] into the cache (one type; rows and heads may be
     strided, as slices of a fused projection are)."""
-    _rows_of(K, "K", batch.rows, cache.kv_heads, cache.head_dim)
-    _rows_of(V, "V", batch.rows, cache.kv_heads, cache.head_dim)
+    rows, heads = batch.rows, cache.kv_heads
+    k_strides = _rows_of(K, "K", rows, heads, cache.head_dim)
+    v_strides = _rows_of(V, "V", rows, heads, cache.head_dim)
     if K.dtype != V.dtype:
         raise TypeError(f"K and V have different dtypes {K.dtype} and {V.dtype}")
     c, device = cache._arg()
     b = batch._arg(device)
     if ws is None:
         ws = new_kv_workspace(cache, batch, None, stream)
-    _check(lib().ttq_kv_write(c, b, *_strided(K, "K", device), *_strided(V, "V", device), _dtype_code(K),
-                              _on(ws, "ws", device), _nbytes(ws), _stream_on(stream, device)), "ttq_kv_write")
+    _check(lib().ttq_kv_write(c, b, *_strided(K, "K", rows, heads, k_strides, device),
+                              *_strided(V, "V", rows, heads, v_strides, device), _dtype_code(K),
+                              _on(ws, "ws", device), ws.nbytes, _stream_on(stream, device)), "ttq_kv_write")
 
 
 def ttq_kv_read(cache, batch, K=None, V=None, dtype=None, ws=None, stream=None):
@@ -829,15 +839,14 @@ def ttq_kv_read(cache, batch, K=None, V=None, dtype=None, ws=None, stream=None):
         raise TypeError(f"unsupported dtype {dtype} (float32, bfloat16 or float16)")
     c, device = cache._arg()
     b = batch._arg(device)
-    shape = (batch.rows, cache.kv_heads, cache.head_dim)
     if K is None:
-        K = _empty(shape, dtype, cache.pages.device, stream)
+        K = _empty_rows(batch.rows, cache.kv_heads, cache.head_dim, dtype, cache.pages.device, stream)
     if V is None:
-        V = torch.empty_like(K) if stream is None else _empty(shape, dtype, cache.pages.device, stream)
+        V = _empty_rows(batch.rows, cache.kv_heads, cache.head_dim, dtype, cache.pages.device, stream)
     if ws is None:
         ws = new_kv_workspace(cache, batch, None, stream)
     _check(lib().ttq_kv_read(c, b, _on(K, "K", device), _on(V, "V", device), _dtype_code(K), _on(ws, "ws", device),
-                             _nbytes(ws), _stream_on(stream, device)), "ttq_kv_read")
+                             ws.nbytes, _stream_on(stream, device)), "ttq_kv_read")
     return K, V
 
 
@@ -846,7 +855,7 @@ def ttq_kv_attention(cache, batch, Q, scale, softcap=0.0, window=0, tree=None, w
     """Y [rows][heads][head_dim]: attention of the batch's rows of Q (strided like K of ttq_kv_write) over the cache,
     causal among a sequence's own rows, or by `tree` (int64 [rows]: bit k of a row's mask is set iff it sees the
     sequence's k-th new row).  softcap: scores are softcap tanh(t / softcap); window: positions seen, 0 for all."""
-    _rows_of(Q, "Q", batch.rows, None, cache.head_dim)
+    q_strides = _rows_of(Q, "Q", batch.rows, None, cache.head_dim)
     heads = Q.shape[1]
     if heads % cache.kv_heads or heads == 0:
         raise ValueError(f"{heads} query heads are not a multiple of the cache's {cache.kv_heads} heads")
@@ -864,15 +873,12 @@ def ttq_kv_attention(cache, batch, Q, scale, softcap=0.0, window=0, tree=None, w
         raise TypeError(f"unsupported dtype {y_dtype} (float32, bfloat16 or float16)")
     c, device = cache._arg()
     b = batch._arg(device)
-    q = _strided(Q, "Q", device)
+    q = _strided(Q, "Q", batch.rows, heads, q_strides, device)
     if Y is None:
-        if stream is None and y_dtype == Q.dtype and Q.is_contiguous():
-            Y = torch.empty_like(Q)
-        else:
-            Y = _empty(Q.shape, y_dtype, Q.device, stream)
+        Y = _empty_rows(batch.rows, heads, cache.head_dim, y_dtype, Q.device, stream)
     if ws is None:
         ws = new_kv_workspace(cache, batch, heads, stream)
     _check(lib().ttq_kv_attention(c, b, *q, _dtype_code(Q), heads, scale, softcap, window, _on(tree, "tree", device),
-                                  _on(Y, "Y", device), _dtype_code(Y), _on(ws, "ws", device), _nbytes(ws),
+                                  _on(Y, "Y", device), _dtype_code(Y), _on(ws, "ws", device), ws.nbytes,
                                   _stream_on(stream, device)), "ttq_kv_attention")
     return Y
