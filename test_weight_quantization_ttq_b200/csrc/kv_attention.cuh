@@ -94,11 +94,16 @@ struct KvAttention {
   // a partial result: accumulators, m and l, m and l of the group merged here
   static constexpr int SLOT = ROWS * (HD + 4);
   // what a segment costs besides its blocks, in blocks: its rows of Q, the
-  // first copies' latency, the merge of the warps' results
+  // first copies' latency, the merge of the warps' results and of the cuts'.
+  // (8 / 16 / 24 / 32 of them: 64 contexts of up to 8192, 8 rows, 98 / 88 /
+  // 89 / 90 us; trees of 24 over 8 contexts of 4099, 32 rows, 128 / 101 / 88 /
+  // 85 us.)
   static constexpr int OVERHEAD = NT == 1 ? 16 : 32;
-  // the least a run has, so that short contexts are not cut into pieces
-  // whose merge costs more than they do
-  static constexpr int LEAST = OVERHEAD + 8;
+  // the least units a run has: few, long runs cost a short context its
+  // latency, many short ones their merge (6 / 10 / 14 / 24: 32 heads of 517
+  // positions 10.1 / 10.6 / 11.2 / 14 us, 8 heads of 2000 14.2 / 13.7 / 12.7 /
+  // 14.4, a chain of 16 over 700 17.9 / 18.1 / 17.9 / 23.3)
+  static constexpr int LEAST = 12;
 };
 
 __device__ __forceinline__ void kv_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
