@@ -63,13 +63,7 @@ __device__ __forceinline__ __half2 u32_as_h2(uint32_t u) {
   return v;
 }
 
-// Two E4M3 codes (low 16 bits) as a binary16 pair, and the two pairs of a
-// word: exact.
-__device__ __forceinline__ uint32_t kv_e4m3x2(uint32_t v) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(v));
-  return h;
-}
+// The two binary16 pairs of a word of four E4M3 codes: exact.
 __device__ __forceinline__ void kv_e4m3x4(uint32_t v, uint32_t& p0, uint32_t& p1) {
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
       "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}" : "=r"(p0), "=r"(p1) : "r"(v));
@@ -161,31 +155,7 @@ __device__ __forceinline__ void kv_copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 8 consecutive elements of a row as float32, and back (rounded to nearest
-// even); all addresses are 16-byte aligned.
-template <int TYPE>
-__device__ __forceinline__ void kv_load8(const void* p, int64_t at, float (&x)[8]) {
-  if constexpr (TYPE == kRowF32) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 a = s[0], b = s[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (TYPE == kRowBF16) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(u32_as_h2(w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-      }
-    }
-  }
-}
+// Two values in one word, rounded to nearest even.
 template <int TYPE>
 __device__ __forceinline__ uint32_t kv_pack2(float a, float b) {
   if constexpr (TYPE == kRowBF16) {
@@ -197,17 +167,4 @@ __device__ __forceinline__ uint32_t kv_pack2(float a, float b) {
     return h2_as_u32(__floats2half2_rn(a, b));
   }
 }
-template <int TYPE>
-__device__ __forceinline__ void kv_store8(void* p, int64_t at, const float (&x)[8]) {
-  if constexpr (TYPE == kRowF32) {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-    d[0] = make_float4(x[0], x[1], x[2], x[3]);
-    d[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
-        make_uint4(kv_pack2<TYPE>(x[0], x[1]), kv_pack2<TYPE>(x[2], x[3]), kv_pack2<TYPE>(x[4], x[5]),
-                   kv_pack2<TYPE>(x[6], x[7]));
-  }
-}
-
 }  // namespace ttq
