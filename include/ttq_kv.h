@@ -53,8 +53,7 @@
  *  - Contents of page_table, kv_len and cu_new are checked on the device.  A
  *    sequence with cu_new decreasing or beyond `rows`, or with rows that are
  *    more than max_new or kv_len, or with kv_len beyond its table, is
- *    skipped, and a
- *    position whose page is not in [0, num_pages) is skipped (written
+ *    skipped, and a position whose page is not in [0, num_pages) is skipped (written
  *    nowhere, read as absent: zeros from ttq_kv_read, not attended to);
  *    both set TTQ_FLAG_BAD_INDEX.
  */
@@ -148,7 +147,9 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
  * are exact, the probabilities times V's scales are rounded to binary16.
  * Scores, maxima and sums are fp32.  Deterministic for given inputs.  ws:
  * ttq_kv_attention_workspace_size(...) bytes, initialised once by
- * ttq_workspace_init.  Flags BAD_INDEX and TIMEOUT. */
+ * ttq_workspace_init (every call leaves its counters at zero) and again
+ * after TIMEOUT; calls that may run at the same time need one each.  Flags
+ * BAD_INDEX and TIMEOUT. */
 ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch, const void* Q,
                             int64_t q_row, int64_t q_head, ttq_dtype dtype, int64_t heads,
                             float scale, float softcap, int64_t window, const uint64_t* tree,
