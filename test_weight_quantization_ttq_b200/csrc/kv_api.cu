@@ -89,14 +89,19 @@ ttq_status status_of(cudaError_t e) { return e == cudaSuccess ? TTQ_OK : TTQ_ERR
 
 }  // namespace
 
-// 8, 16 or 32 query rows per tile: the fewest that hold a sequence's rows of
-// one key/value head, since rows of a tile that are not there cost as much as
-// those that are, while every further tile reads and unpacks the codes again.
-// Heads of 256 channels stop at 16 (their accumulators fill the registers).
+// 8, 16, 24 or 32 query rows per tile: the fewest that hold a sequence's rows
+// of one key/value head, since rows of a tile that are not there cost as much
+// as those that are, while every further tile reads and unpacks the codes
+// again; of more rows than 32 tiles of 24 if that makes no more of them.  (24
+// against 32: 16 sequences of 4000, 24 rows, 44.7 and 50.3 us; 16 of up to
+// 2048, 48 rows of heads of 64, 24.7 and 28.2.  24 against 32 at 192 rows,
+// which makes 8 tiles instead of 6: 94 and 83.  16 against 32 at 256: 188 and
+// 165.)  Heads of 256 channels stop at 16 (their accumulators fill the
+// registers).
 KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows) {
   KvAttentionPlan p = {};
   if (!format_built(hd, bits, group)) return p;
-  p.nt = tile_rows <= 8 ? 1 : (tile_rows <= 16 || hd == 256) ? 2 : 4;
+  p.nt = tile_rows <= 8 ? 1 : (tile_rows <= 16 || hd == 256) ? 2 : (tile_rows + 23) / 24 == (tile_rows + 31) / 32 ? 3 : 4;
   const int ctas = hd == 64    ? kv_attention_ctas_hd64(bits, group, p.nt)
                    : hd == 128 ? kv_attention_ctas_hd128(bits, group, p.nt)
                                : kv_attention_ctas_hd256(bits, group, p.nt);

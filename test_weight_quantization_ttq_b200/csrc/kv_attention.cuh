@@ -1021,8 +1021,10 @@ bool kv_with_format(int bits, int group, int nt, Fn&& f) {
   auto tiles = [&](auto BITSc, auto NGc) {
     if (nt == 1) return f(BITSc, NGc, std::integral_constant<int, 1>{}), true;
     if (nt == 2) return f(BITSc, NGc, std::integral_constant<int, 2>{}), true;
-    if constexpr (HD <= 128)
+    if constexpr (HD <= 128) {
+      if (nt == 3) return f(BITSc, NGc, std::integral_constant<int, 3>{}), true;
       if (nt == 4) return f(BITSc, NGc, std::integral_constant<int, 4>{}), true;
+    }
     return false;
   };
   auto groups = [&](auto BITSc) {

@@ -92,6 +92,14 @@ def test_trees_of_every_format(hd, bits, group, n, per):
     check(case, per=per, masks=_trees(new, n))
 
 
+@pytest.mark.parametrize("hd,bits,group", FORMATS)
+def test_trees_of_every_format_in_wide_tiles(hd, bits, group):
+    """32 rows a tile (16 with heads of 256), one tile and its rows full, ragged and absent."""
+    new = [8, 3, 0, 7]
+    case = R.Case(new, [50, 3, 33, 71], heads=2, hd=hd, bits=bits, group=group, page=48, seed=hd + bits + group + 1)
+    check(case, per=4, masks=_trees(new, 2))
+
+
 @pytest.mark.parametrize("scheme,bits", [(R.SYM, 4), (R.SYM, 2), (R.ASYM, 4)])
 @pytest.mark.parametrize("dtype,y_dtype", [(f16, None), (bf16, f32), (f32, None), (f32, bf16)])
 def test_schemes_and_types(scheme, bits, dtype, y_dtype):
