@@ -97,16 +97,20 @@ ttq_status status_of(cudaError_t e) { return e == cudaSuccess ? TTQ_OK : TTQ_ERR
 // 2048, 48 rows of heads of 64, 24.7 and 28.2.  24 against 32 at 192 rows,
 // which makes 8 tiles instead of 6: 94 and 83.  16 against 32 at 256: 188 and
 // 165.)  Heads of 256 channels stop at 16 (their accumulators fill the
-// registers).
+// registers).  The tiles of 256 rows of kv_attention_wide.cuh (nt = 16), of
+// heads up to 128 in one or two groups, where each stands for 6 tiles of 32
+// or more: trees of 24 with 192 rows 76 us (6 tiles 83), trees of 64 with
+// 256 rows 138 (8 tiles 165); one of fewer rows costs as much, so that 5
+// would be about even.
 KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows) {
   KvAttentionPlan p = {};
   if (!format_built(hd, bits, group)) return p;
-  p.nt = tile_rows <= 8 ? 1 : (tile_rows <= 16 || hd == 256) ? 2 : (tile_rows + 23) / 24 == (tile_rows + 31) / 32 ? 3 : 4;
+  p.nt = hd <= 128 && hd / group <= 2 && (tile_rows + 31) / 32 >= 6 * ((tile_rows + 255) / 256) ? 16 : tile_rows <= 8 ? 1 : (tile_rows <= 16 || hd == 256) ? 2 : (tile_rows + 23) / 24 == (tile_rows + 31) / 32 ? 3 : 4;
   const int ctas = hd == 64    ? kv_attention_ctas_hd64(bits, group, p.nt)
                    : hd == 128 ? kv_attention_ctas_hd128(bits, group, p.nt)
                                : kv_attention_ctas_hd256(bits, group, p.nt);
   p.grid = ctas * kKvPlanSMs;
-  p.slot_floats = static_cast<int64_t>(8 * p.nt) * (hd + 4);
+  p.slot_floats = static_cast<int64_t>(p.nt == 16 ? 256 : 8 * p.nt) * (hd + 4);
   p.part_bytes = static_cast<int64_t>(p.grid) * 2 * p.slot_floats * 4;
   return p;
 }

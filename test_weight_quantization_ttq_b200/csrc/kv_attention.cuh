@@ -254,33 +254,71 @@ struct KvRuns {
   }
 };
 
+// Which of block blk's 16 tokens a row sees (bit t): of the old tokens all, of
+// the new ones those of its mask, with a window those less than `window` back.
+__device__ __forceinline__ uint32_t kv_visible(const KvAttentionArgs& a, int row0, int old, int kv, int blk, uint64_t mask,
+                                               int pos) {
+  const int p0 = blk * 16, there = min(kv - p0, 16), j0 = old - p0;
+  auto below = [](int64_t n) { return n <= 0 ? 0u : n >= 16 ? 0xFFFFu : (1u << n) - 1u; };
+  uint32_t before = below(j0), since = 0;         // of the old tokens, of the new ones
+  if (j0 < 16) since = static_cast<uint32_t>(j0 >= 0 ? mask << j0 : mask >> min(-j0, 63)) & ~below(j0);
+  if (a.window > 0) {
+    const uint32_t far = below(pos - a.window + 1 - p0);
+    before &= ~far;
+    if (a.tree == nullptr) {
+      since &= ~far;
+    } else {
+#pragma unroll 1
+      for (int j = max(j0, 0); j < there; ++j) {
+        const int k_new = j - j0;
+        if (pos - old - __popcll(a.tree[row0 + k_new] & ~(1ull << k_new)) >= a.window) since &= ~(1u << j);
+      }
+    }
+  }
+  return (before | since) & below(there);
+}
+
+}  // namespace ttq
+
+#include "kv_attention_wide.cuh"
+
+namespace ttq {
+
+// A block's shape: NT tiles of 8 rows a warp's products, or (NT = 16) the 128 rows of kv_attention_wide.cuh.
 template <int HD, int BITS, int NG, int NT>
-__global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAttention<HD, BITS, NG, NT>::CTAS)
-    kv_attention_kernel(const KvAttentionArgs a) {
+struct KvShape {
   using A = KvAttention<HD, BITS, NG, NT>;
+};
+template <int HD, int BITS, int NG>
+struct KvShape<HD, BITS, NG, 16> {
+  using A = KvWide<HD, BITS, NG>;
+};
+
+template <int HD, int BITS, int NG, int NT>
+__global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<HD, BITS, NG, NT>::A::CTAS)
+    kv_attention_kernel(const KvAttentionArgs a) {
+  using A = typename KvShape<HD, BITS, NG, NT>::A;
   using F = typename A::F;
-  constexpr int W = A::W, ROWS = A::ROWS, KS = A::KS, MT = A::MT, STAGES = A::STAGES, OV = A::OVERHEAD;
-  constexpr int PW = F::PIECE / 4;              // words of a lane's piece
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t all_bars[W * STAGES];
-  __shared__ int all_absent[W * STAGES];        // the stage's block has no page
-  __shared__ float warp_m[W][ROWS], warp_l[W][ROWS];
+  constexpr bool WIDE = NT == 16;
+  constexpr int W = A::W, ROWS = A::ROWS, OV = A::OVERHEAD;
+  constexpr int PARTS = WIDE ? 1 : W;           // accumulators of a part: the warps', or the block's
+  extern __shared__ __align__(1024) uint8_t dynamic_smem[];
+  // (operands of tcgen05 stand on 1024-byte boundaries)
+  uint8_t* const smem = WIDE ? dynamic_smem + (-smem_addr(dynamic_smem) & 1023u) : dynamic_smem;
+  __shared__ __align__(8) uint64_t all_bars[WIDE ? 1 : W * A::STAGES];
+  __shared__ int all_absent[WIDE ? 1 : W * A::STAGES];   // the stage's block has no page
+  __shared__ __align__(8) KvWideBars wide_bars;
+  __shared__ uint32_t tmem_at;
+  __shared__ float warp_m[PARTS][ROWS], warp_l[PARTS][ROWS];
   __shared__ KvRuns runs_s;
   __shared__ int abort_flag, last_flag;
   const KvGeometry& g = a.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int gr = lane >> 2, tq = lane & 3;      // row group and quarter of the MMA fragments
-  uint8_t* ring = smem + warp * A::WARP_BYTES;
-  uint32_t* qfrag = reinterpret_cast<uint32_t*>(smem + W * A::WARP_BYTES);
-  uint64_t* row_mask = reinterpret_cast<uint64_t*>(smem + W * A::WARP_BYTES + A::QFRAG);
+  uint64_t* row_mask = reinterpret_cast<uint64_t*>(smem + PARTS * A::WARP_BYTES + A::QFRAG);
   float* q_factor = reinterpret_cast<float*>(row_mask + ROWS);   // t = <row, (c - z) s> * q_factor
   int* row_pos = reinterpret_cast<int*>(q_factor + ROWS);
-  float* q_sum = reinterpret_cast<float*>(row_pos + ROWS);       // [NG][ROWS] sums of a row's group
-  float* q_off = q_sum + NG * ROWS;                              // the same with the fields' offsets as weights
-  uint64_t* bars = all_bars + warp * STAGES;
-  int* absent = all_absent + warp * STAGES;
   // {end of its work in blocks of one head (56 bits), n (8 bits); kv; row0}
-  int4* seqs = reinterpret_cast<int4*>(smem + A::SMEM);
+  int4* seqs = reinterpret_cast<int4*>(dynamic_smem + A::SMEM);
   auto pack = [](int64_t end, int n, int kv, int row0) {
     return make_int4(static_cast<int>(end), static_cast<int>((end >> 32) & 0xFFFFFF) | n << 24, kv, row0);
   };
@@ -289,8 +327,21 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
   };
 
   allow_dependents_launch();
-  if (lane == 0) {
-    for (int s = 0; s < STAGES; ++s) mbar_init(&bars[s], 1);
+  if constexpr (WIDE) {
+    if (tid == 0) {
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&wide_bars.op_full[s], 8);
+        mbar_init(&wide_bars.op_free[s], 1);
+        mbar_init(&wide_bars.s_full[s], 1);
+        mbar_init(&wide_bars.s_free[s], 8);
+      }
+      mbar_init(&wide_bars.p_full, 8);
+      mbar_init(&wide_bars.pv_done, 1);
+      mbar_init(&wide_bars.drain, 1);
+      fence_barrier_init();
+    }
+  } else if (lane == 0) {
+    for (int s = 0; s < A::STAGES; ++s) mbar_init(&all_bars[warp * A::STAGES + s], 1);
     fence_barrier_init();
   }
   if (tid == 0) abort_flag = 0;
@@ -370,7 +421,27 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
   }
 
   const KvMagic<BITS> magic;
-  int turn = 0;                                 // blocks waited for so far: stage and parity of the ring
+  int turn = 0;                                 // blocks (wide: steps) waited for so far: stage and parity of the ring
+  if constexpr (WIDE) {
+    if (warp == W - 1) {
+      tmem_alloc(&tmem_at, A::COLUMNS);
+      tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+  }
+  // nothing of tensor memory is in use any more
+  auto leave = [&]() {
+    if constexpr (WIDE) {
+      tc_fence_before_sync();
+      __syncthreads();
+      if (warp == W - 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_at, A::COLUMNS);
+      }
+    }
+  };
   for (bool started = false; x < x1; started = true) {
     if (started && left == 0) {                 // the next segment
       if (++seg.tile == tiles) {
@@ -387,18 +458,53 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     left -= take;
     const int part = seg.blocks - static_cast<int>(left < seg.blocks ? left : seg.blocks) - from;
     if (part == 0) continue;
+    const int old = seg.kv - seg.n;             // positions before the new ones
+    const int R = seg.n * a.per, r0 = seg.tile * ROWS;
+    const int here = min(R - r0, ROWS);         // rows of the tile
+    const float factor = a.scale * (a.cap > 0.f ? kv_rcp(a.cap) : kKvLog2e);
+    // of `count` blocks from blk0 on, [plain0, plain1) need no masks: not those
+    // that the window of the last new token does not cover, nor those that
+    // reach the new tokens
+    auto unmasked = [&](int blk0, int count, int& plain0, int& plain1) {
+      plain0 = 0;
+      if (a.window > 0 && seg.kv > a.window) {
+        const int64_t past = static_cast<int64_t>(seg.kv) - a.window;   // p >= past is in every row's window
+        const int64_t need = (past + 15) / 16 - blk0;                   // first block wholly in it
+        plain0 = need <= 0 ? 0 : need >= count ? count : static_cast<int>(need);
+      }
+      plain1 = (old >> 4) - blk0;                                       // blocks before the new tokens
+    };
+    if constexpr (WIDE) {
+      float* tables = reinterpret_cast<float*>(row_pos + ROWS);
+      KvWidePart<HD, BITS, NG> p{a, wide_bars, &abort_flag, smem, row_mask, q_factor, row_pos, tables,
+                                 tables + 2 * NG * A::STEP, reinterpret_cast<int*>(tables + 4 * NG * A::STEP), tmem_at};
+      p.b = seg.b, p.h = seg.h, p.row0 = seg.row0, p.n = seg.n, p.kv = seg.kv, p.old = old;
+      p.blk0 = seg.first + from, p.count = part, p.steps = (part + 3) / 4, p.here = here, p.r0 = r0, p.turn0 = turn;
+      unmasked(p.blk0, part, p.plain0, p.plain1);
+      p.rows(tid, factor);
+      __syncthreads();
+      if (warp < 8) p.softmax(tid, &warp_m[0][tid], &warp_l[0][tid]);
+      else p.unpack(warp - 8);
+      turn += p.steps;
+    } else {
+    constexpr int KS = A::KS, MT = A::MT, STAGES = A::STAGES;
+    constexpr int PW = F::PIECE / 4;            // words of a lane's piece
+    const int gr = lane >> 2, tq = lane & 3;    // row group and quarter of the MMA fragments
+    uint8_t* ring = smem + warp * A::WARP_BYTES;
+    uint32_t* qfrag = reinterpret_cast<uint32_t*>(smem + W * A::WARP_BYTES);
+    float* q_sum = reinterpret_cast<float*>(row_pos + ROWS);       // [NG][ROWS] sums of a row's group
+    float* q_off = q_sum + NG * ROWS;                              // the same with the fields' offsets as weights
+    uint64_t* bars = all_bars + warp * STAGES;
+    int* absent = all_absent + warp * STAGES;
     // of these this warp's: [blk0, blk0 + count)
     const int mine0 = static_cast<int>(static_cast<int64_t>(part) * warp / W);
     const int count = static_cast<int>(static_cast<int64_t>(part) * (warp + 1) / W) - mine0;
     const int blk0 = seg.first + from + mine0;
-    const int old = seg.kv - seg.n;             // positions before the new ones
-    const int R = seg.n * a.per, r0 = seg.tile * ROWS;
 
     // ---- the tile's rows, 2 NT to a warp: their loads from Q are on their
     // way while the pages are looked up and the copies start
     constexpr int E = HD / 32;                  // consecutive channels of a lane
     constexpr int OWN = ROWS / W;               // rows that a warp prepares
-    const int here = min(R - r0, ROWS);         // rows of the tile
     const bool wide = a.q_type == kRowF32;
     uint32_t raw[OWN][E] = {};                  // E words of float32, E / 2 of 16-bit elements
     {
@@ -462,7 +568,6 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       float dk[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) dk[e] = a.Dk != nullptr ? __ldg(a.Dk + seg.h * HD + lane * E + e) : 1.f;
-      const float factor = a.scale * (a.cap > 0.f ? kv_rcp(a.cap) : kKvLog2e);
 #pragma unroll
       for (int k = 0; k < OWN; ++k) {
         const int r = OWN * warp + k;
@@ -523,21 +628,15 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
     bool all_seen = false;                      // all columns of all lanes
     float vf = 1.2676506e30f;                   // 2^-E; at first 2^100, so that any scale lowers it
     float zs[A::VRAW ? NG : 1][4] = {};         // sums of p s (offset + z) 2^-E per group
-    // blocks [plain0, plain1) need no masks: not those that the window of the
-    // last new token does not cover, nor those that reach the new tokens
-    int plain0 = 0;
-    if (a.window > 0 && seg.kv > a.window) {
-      const int64_t past = static_cast<int64_t>(seg.kv) - a.window;   // p >= past is in every row's window
-      const int64_t need = (past + 15) / 16 - blk0;                   // first block wholly in it
-      plain0 = need <= 0 ? 0 : need >= count ? count : static_cast<int>(need);
-    }
-    const int plain1 = (old >> 4) - blk0;                             // blocks before the new tokens
+    int plain0, plain1;
+    unmasked(blk0, count, plain0, plain1);
     const uint32_t q_frags = smem_addr(qfrag) + lane * 16;
 
 #pragma unroll 1
     for (int done = 0; done < count; ++done) {
       const int stage = (turn0 + done) % STAGES, blk = blk0 + done;
-      if (!mbar_wait(&bars[stage], ((turn0 + done) / STAGES) & 1, &abort_flag)) {
+      // (the lanes go on together or not at all)
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars[stage], ((turn0 + done) / STAGES) & 1, &abort_flag))) {
         // a copy did not arrive in time: say so and wait, with the same limit,
         // for the copies still in flight; the results are not right any more
         if (lane == 0) {
@@ -652,26 +751,9 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       // -- masks: lane r finds which of the block's tokens row r sees; tokens
       // that are not there count for nothing, whatever their bytes are
       if (masked) {
-        const int p0 = blk * 16, there = gone ? 0 : min(seg.kv - p0, 16), j0 = old - p0;
-        auto below = [](int64_t n) { return n <= 0 ? 0u : n >= 16 ? 0xFFFFu : (1u << n) - 1u; };
-        const uint64_t mask = row_mask[lane % ROWS];
-        const int pos = row_pos[lane % ROWS];
-        uint32_t before = below(j0), since = 0;   // of the old tokens, of the new ones
-        if (j0 < 16) since = static_cast<uint32_t>(j0 >= 0 ? mask << j0 : mask >> min(-j0, 63)) & ~below(j0);
-        if (a.window > 0) {
-          const uint32_t far = below(pos - a.window + 1 - p0);
-          before &= ~far;
-          if (a.tree == nullptr) {
-            since &= ~far;
-          } else {
-#pragma unroll 1
-            for (int j = max(j0, 0); j < there; ++j) {
-              const int k_new = j - j0;
-              if (pos - old - __popcll(a.tree[seg.row0 + k_new] & ~(1ull << k_new)) >= a.window) since &= ~(1u << j);
-            }
-          }
-        }
-        const uint32_t vis = (before | since) & below(there);
+        const int there = gone ? 0 : min(seg.kv - blk * 16, 16);
+        const uint32_t vis =
+            gone ? 0u : kv_visible(a, seg.row0, old, seg.kv, blk, row_mask[lane % ROWS], row_pos[lane % ROWS]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -858,6 +940,7 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
           }
         }
     }
+    }
     __syncthreads();
     const bool failed = *static_cast<volatile int*>(&abort_flag) != 0;
     const bool whole = part == seg.blocks;
@@ -875,9 +958,9 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
       float mx = warp_m[0][r], sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 1; w < W; ++w) mx = fmaxf(mx, warp_m[w][r]);
+      for (int w = 1; w < PARTS; ++w) mx = fmaxf(mx, warp_m[w][r]);
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
+      for (int w = 0; w < PARTS; ++w) {
         const float f = kv_exp2(warp_m[w][r] - mx);
         const float4 v = *reinterpret_cast<const float4*>(smem + w * A::WARP_BYTES + (r * A::LDO + ch) * 4);
         sum = fmaf(warp_l[w][r], f, sum);
@@ -1000,10 +1083,19 @@ __global__ void __launch_bounds__(KvAttention<HD, BITS, NG, NT>::W * 32, KvAtten
         }
       }
     }
-    if (failed) return;                         // (set before the barrier above: the same for all threads)
+    if (failed) {                               // (set before the barrier above: the same for all threads)
+      if (WIDE && tid == 8 * 32) {              // no product is under way when tensor memory is freed
+        int never = 0;
+        mma_commit(&wide_bars.drain);
+        mbar_wait(&wide_bars.drain, 0, &never);
+      }
+      leave();
+      return;
+    }
     fence_proxy_async_smem();                   // the regions are the copies' again
     __syncthreads();
   }
+  leave();
 }
 
 // One head size's kernels (a source file each).
@@ -1021,6 +1113,8 @@ bool kv_with_format(int bits, int group, int nt, Fn&& f) {
   auto tiles = [&](auto BITSc, auto NGc) {
     if (nt == 1) return f(BITSc, NGc, std::integral_constant<int, 1>{}), true;
     if (nt == 2) return f(BITSc, NGc, std::integral_constant<int, 2>{}), true;
+    if constexpr (HD <= 128 && decltype(NGc)::value <= 2)
+      if (nt == 16) return f(BITSc, NGc, std::integral_constant<int, 16>{}), true;
     if constexpr (HD <= 128) {
       if (nt == 3) return f(BITSc, NGc, std::integral_constant<int, 3>{}), true;
       if (nt == 4) return f(BITSc, NGc, std::integral_constant<int, 4>{}), true;
@@ -1045,7 +1139,7 @@ template <int HD>
 int kv_attention_ctas(int bits, int group, int nt) {
   int n = 0;
   kv_with_format<HD>(bits, group, nt, [&](auto B, auto G, auto N) {
-    n = KvAttention<HD, decltype(B)::value, decltype(G)::value, decltype(N)::value>::CTAS;
+    n = KvShape<HD, decltype(B)::value, decltype(G)::value, decltype(N)::value>::A::CTAS;
   });
   return n;
 }
@@ -1056,7 +1150,7 @@ cudaError_t kv_attention_launch(const KvAttentionArgs& a, int bits, int group, c
   cudaError_t e = cudaErrorInvalidValue;
   kv_with_format<HD>(bits, group, p.nt, [&](auto Bc, auto Gc, auto Nc) {
     constexpr int BITS = decltype(Bc)::value, NG = decltype(Gc)::value, NT = decltype(Nc)::value;
-    using A = KvAttention<HD, BITS, NG, NT>;
+    using A = typename KvShape<HD, BITS, NG, NT>::A;
     auto* kernel = kv_attention_kernel<HD, BITS, NG, NT>;
     const int smem = A::SMEM + 16 * a.g.batch;
     static std::atomic<uint64_t> set{0};

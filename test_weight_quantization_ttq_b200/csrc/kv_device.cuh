@@ -143,6 +143,25 @@ __device__ __forceinline__ float kv_max_nan(float a, float b) {
   return r;
 }
 
+// N words of a lane's half from their pieces.
+template <typename F, int N>
+__device__ __forceinline__ void kv_load_codes(const uint8_t* part, int lane, int half, uint32_t (&w)[N]) {
+  constexpr int PW = F::PIECE / 4;
+#pragma unroll
+  for (int c = 0; c < N / PW; ++c) {
+    const uint8_t* p = part + (c * 2 + half) * 32 * F::PIECE + lane * F::PIECE;
+    if constexpr (PW == 1) {
+      w[c] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (PW == 2) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[2 * c] = u.x, w[2 * c + 1] = u.y;
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      w[4 * c] = u.x, w[4 * c + 1] = u.y, w[4 * c + 2] = u.z, w[4 * c + 3] = u.w;
+    }
+  }
+}
+
 // 16 bytes global -> shared, asynchronously, past the L1 cache; zeros where
 // `there` is false (src is not read then).  Copies since the last commit form
 // a group; wait<N> returns when all but this thread's last N groups are done.

@@ -4,25 +4,6 @@
 namespace ttq {
 namespace {
 
-// N words of a lane's half from their pieces.
-template <typename F, int N>
-__device__ __forceinline__ void load_code_words(const uint8_t* part, int lane, int half, uint32_t (&w)[N]) {
-  constexpr int PW = F::PIECE / 4;
-#pragma unroll
-  for (int c = 0; c < N / PW; ++c) {
-    const uint8_t* p = part + (c * 2 + half) * 32 * F::PIECE + lane * F::PIECE;
-    if constexpr (PW == 1) {
-      w[c] = *reinterpret_cast<const uint32_t*>(p);
-    } else if constexpr (PW == 2) {
-      const uint2 u = *reinterpret_cast<const uint2*>(p);
-      w[2 * c] = u.x, w[2 * c + 1] = u.y;
-    } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      w[4 * c] = u.x, w[4 * c + 1] = u.y, w[4 * c + 2] = u.z, w[4 * c + 3] = u.w;
-    }
-  }
-}
-
 // Two codes' values less the zero, as float32: pair p of kv_int_pairs, or two E4M3.
 __device__ __forceinline__ float2 floats_of(uint32_t p) { return __half22float2(u32_as_h2(p)); }
 
@@ -72,7 +53,7 @@ __global__ void __launch_bounds__(kThreads, HD == 256 || TYPE == kRowF32 ? 2 : 3
       uint32_t w[2][WORDS], pair[2][2][NG];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        load_code_words<F, WORDS>(part, lane, r, w[r]);
+        kv_load_codes<F>(part, lane, r, w[r]);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll

@@ -354,3 +354,80 @@ def test_more_new_rows_than_a_mask_holds_are_refused():
     with pytest.raises(ttq.TTQError) as e:
         ttq.ttq_kv_attention(cache, big, torch.zeros((1, 2, 64), dtype=bf16, device="cuda"), 1.0)
     assert e.value.status == ttq.TTQ_ERR_UNSUPPORTED
+
+
+WIDE = [(hd, b, g) for hd, b, g in FORMATS if hd <= 128 and hd // g <= 2]
+
+
+@pytest.mark.parametrize("hd,bits,group", WIDE)
+@pytest.mark.parametrize("tree", [False, True])
+def test_tiles_of_256_rows_of_every_format(hd, bits, group, tree):
+    """Full, ragged and nearly empty tiles of rows; lengths around a step's 64 tokens."""
+    new = [64, 61, 0, 3, 64]
+    case = R.Case(new, [64, 127, 20, 67, 200], heads=1, hd=hd, bits=bits, group=group, page=32, seed=hd + bits + group)
+    check(case, per=4, masks=_trees(new, 5) if tree else None)
+
+
+@pytest.mark.parametrize("kw", [dict(cap=7.0), dict(window=1), dict(window=50), dict(window=130), dict(dtype=f32),
+                                dict(dtype=f16, y_dtype=f32), dict(stat=True), dict(scheme=R.SYM), dict(rows=5),
+                                dict(per=5), dict(per=7), dict(q_scale=3.0), dict(small=True)], ids=str)
+def test_tiles_of_256_rows(kw):
+    kw = dict(kw)
+    new = [48, 64, 50]
+    per = kw.pop("per", 4)
+    small = kw.pop("small", False)
+    case = R.Case(new, [300, 64, 131], heads=2, hd=128, bits=4, group=64, page=16, seed=31, stat=kw.pop("stat", False),
+                  scheme=kw.pop("scheme", None), extra_rows=kw.pop("rows", 0),
+                  scale_of=(lambda which, b: 1e-3 * 40.0 ** b) if small else (lambda which, b: 1.0))
+    check(case, per=per, masks=_trees(new, 6), **kw)
+
+
+def test_wide_tiles_of_long_contexts_are_cut_and_joined():
+    """Enough steps that a segment's parts are many, their maxima apart; every time the same bits."""
+    case = R.Case([64], [7000], heads=1, hd=64, bits=4, group=64, page=64, seed=32)
+    Q = (torch.randn(64, 4, 64, generator=torch.Generator().manual_seed(33)) * 3).to(bf16)
+    Y = check(case, per=4, Q=Q)
+    for _ in range(3):
+        assert torch.equal(check(case, per=4, Q=Q), Y)
+
+
+def test_wide_tiles_skip_what_is_not_there():
+    """NaN scales in sight of some rows, pages that are not the cache's, sequences that are not valid."""
+    case = R.Case([64, 64], [150, 100], heads=1, hd=128, bits=4, group=128, page=16, seed=34)
+    masks = [1 << i for i in range(64)] * 2       # every new token sees the old ones and itself
+    cache, batch = case.on_gpu()
+    Q = torch.randn(128, 4, 128, generator=torch.Generator().manual_seed(35)).to(bf16).cuda()
+    tree = _signed(masks).cuda()
+    ws = ttq.new_kv_workspace(cache, batch, 4)
+    good = ttq.ttq_kv_attention(cache, batch, Q, 0.1, tree=tree, ws=ws)
+    # the last new token of sequence 0: a NaN key and value, which it alone sees
+    nan = torch.full((1, 1, 128), float("nan"), dtype=bf16, device="cuda")
+    one = ttq.KVBatch(batch.page_table[:1], batch.kv_len[:1], torch.tensor([0, 1], dtype=torch.int32, device="cuda"), 1, 1)
+    ttq.ttq_kv_write(cache, one, nan, nan)
+    Y = ttq.ttq_kv_attention(cache, batch, Q, 0.1, tree=tree, ws=ws)
+    assert bool(Y[63].isnan().all())
+    keep = [r for r in range(128) if r != 63]
+    assert torch.equal(Y[keep], good[keep])
+    assert ttq.ttq_get_status(ws) == (ttq.TTQ_OK, 0)
+    # a page of sequence 1's old tokens: as if its positions were not there
+    batch.page_table[1, 1] = 10 ** 8
+    Y = ttq.ttq_kv_attention(cache, batch, Q, 0.1, tree=tree, ws=ws)
+    torch.cuda.synchronize()
+    assert ttq.ttq_get_status(ws)[1] == ttq.TTQ_FLAG_BAD_INDEX
+    assert torch.equal(Y[:63], good[:63])
+    K, V = case.sequence(1)
+    see = R.visible(64, 100, 0, masks[64:])
+    see[:, 16:32] = False
+    y, bound = R.attention(K, V, Q[64:].cpu().double().numpy(), float(np.float32(0.1)), see)
+    got = Y[64:].cpu().double().numpy()
+    assert (np.abs(got - y) <= bound + (np.abs(y) + bound) * 2.0 ** -8 + 1e-5).all()
+    # a length beyond the table: its rows stay
+    batch.kv_len[1] = 10 ** 6
+    Y = torch.full_like(Q, 5.0)
+    ttq.ttq_kv_attention(cache, batch, Q, 0.1, tree=tree, ws=ws, Y=Y)
+    assert bool((Y[64:] == 5).all())
+    # (sequence 0 may be cut at other blocks now, so that its results are the same to their bound, not to the bit)
+    K, V = case.sequence(0)
+    y, bound = R.attention(K, V, Q[:64].cpu().double().numpy(), float(np.float32(0.1)), R.visible(64, 150, 0, masks[:64]))
+    got = Y[:63].cpu().double().numpy()
+    assert (np.abs(got - y[:63]) <= bound[:63] + (np.abs(y[:63]) + bound[:63]) * 2.0 ** -8 + 1e-5).all()
