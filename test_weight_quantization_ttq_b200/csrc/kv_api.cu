@@ -105,7 +105,11 @@ ttq_status status_of(cudaError_t e) { return e == cudaSuccess ? TTQ_OK : TTQ_ERR
 KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows) {
   KvAttentionPlan p = {};
   if (!format_built(hd, bits, group)) return p;
-  p.nt = hd <= 128 && hd / group <= 2 && (tile_rows + 31) / 32 >= 6 * ((tile_rows + 255) / 256) ? 16 : tile_rows <= 8 ? 1 : (tile_rows <= 16 || hd == 256) ? 2 : (tile_rows + 23) / 24 == (tile_rows + 31) / 32 ? 3 : 4;
+  const int64_t tiles32 = (tile_rows + 31) / 32, tiles256 = (tile_rows + 255) / 256;
+  if (hd <= 128 && hd / group <= 2 && tiles256 > 0 && tiles32 >= 6 * tiles256) p.nt = 16;
+  else if (tile_rows <= 8) p.nt = 1;
+  else if (tile_rows <= 16 || hd == 256) p.nt = 2;
+  else p.nt = (tile_rows + 23) / 24 == tiles32 ? 3 : 4;
   const int ctas = hd == 64    ? kv_attention_ctas_hd64(bits, group, p.nt)
                    : hd == 128 ? kv_attention_ctas_hd128(bits, group, p.nt)
                                : kv_attention_ctas_hd256(bits, group, p.nt);
