@@ -89,6 +89,12 @@ ttq_status status_of(cudaError_t e) { return e == cudaSuccess ? TTQ_OK : TTQ_ERR
 
 }  // namespace
 
+// Tiles of 256 rows pay where there is work for them: the blocks that the
+// batch's sequences may have, by the width of its page table (32 heads over 8,
+// trees of 48: 4000 blocks 54 us, 42 in tiles of 32; 8000 blocks 69 and 66;
+// trees of 64: 4000 blocks 60 and 50, 16448 blocks 138 and 165).
+constexpr int64_t kWideBlocks = 8192;
+
 // 8, 16, 24 or 32 query rows per tile: the fewest that hold a sequence's rows
 // of one key/value head, since rows of a tile that are not there cost as much
 // as those that are, while every further tile reads and unpacks the codes
@@ -102,11 +108,11 @@ ttq_status status_of(cudaError_t e) { return e == cudaSuccess ? TTQ_OK : TTQ_ERR
 // or more: trees of 24 with 192 rows 76 us (6 tiles 83), trees of 64 with
 // 256 rows 138 (8 tiles 165); one of fewer rows costs as much, so that 5
 // would be about even.
-KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows) {
+KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows, int64_t blocks) {
   KvAttentionPlan p = {};
   if (!format_built(hd, bits, group)) return p;
   const int64_t tiles32 = (tile_rows + 31) / 32, tiles256 = (tile_rows + 255) / 256;
-  if (hd <= 128 && hd / group <= 2 && tiles256 > 0 && tiles32 >= 6 * tiles256) p.nt = 16;
+  if (hd <= 128 && hd / group <= 2 && tiles256 > 0 && tiles32 >= 6 * tiles256 && blocks >= kWideBlocks) p.nt = 16;
   else if (tile_rows <= 8) p.nt = 1;
   else if (tile_rows <= 16 || hd == 256) p.nt = 2;
   else p.nt = (tile_rows + 23) / 24 == tiles32 ? 3 : 4;
@@ -172,9 +178,16 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
                                        int64_t kv_heads, int64_t max_new) {
   if (kv_heads < 1 || heads < kv_heads || heads % kv_heads != 0 || heads > 65535) return 0;
   if (max_new < 0 || max_new > kKvMaxNew) return 0;
-  const KvAttentionPlan p = kv_attention_plan(head_dim, bits, group, max_new * (heads / kv_heads));
-  if (p.grid == 0) return 0;
-  return kKvHeader + p.part_bytes;
+  // the most of what any context lengths and any fewer rows take: the plans of
+  // every width of tile up to the rows' own
+  const int64_t tile_rows = max_new * (heads / kv_heads);
+  int64_t most = 0;
+  for (const int64_t rows : {8, 16, 24, 32, 256}) {
+    const KvAttentionPlan p = kv_attention_plan(head_dim, bits, group, tile_rows < rows ? tile_rows : rows, INT64_MAX);
+    if (p.grid == 0) return 0;
+    if (p.part_bytes > most) most = p.part_bytes;
+  }
+  return kKvHeader + most;
 }
 
 ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch, const void* Q,
@@ -195,7 +208,9 @@ ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch
   if (batch->rows == 0 || batch->batch == 0 || batch->max_new == 0) return TTQ_OK;
   if (Q == nullptr || Y == nullptr) return TTQ_ERR_INVALID_ARG;
   const int per = static_cast<int>(heads / cache->kv_heads);
-  const KvAttentionPlan p = kv_attention_plan(cache->head_dim, cache->bits, cache->group, batch->max_new * per);
+  const int64_t longest = batch->table_stride * a.g.page_blocks;   // blocks that a sequence may have (below 2^44)
+  const int64_t blocks = batch->batch * cache->kv_heads * (longest < (1 << 27) ? longest : 1 << 27);
+  const KvAttentionPlan p = kv_attention_plan(cache->head_dim, cache->bits, cache->group, batch->max_new * per, blocks);
   a.Dk = cache->D_k_rsqrt;
   a.Dv = cache->D_v_rsqrt;
   a.Q = Q;

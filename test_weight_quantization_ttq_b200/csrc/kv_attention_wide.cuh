@@ -55,8 +55,10 @@ struct KvWide {
   static constexpr int MOST = 13;                   // results merged at a time: there are 148 at most
   static_assert(ROWS * LDO * 4 <= REGION && (MOST * (2 * ROWS + 1) + ROWS) * 4 <= REGION, "what the region holds");
   static constexpr int SLOT = ROWS * (HD + 4);
-  // what a segment costs besides its blocks, in blocks, and the least a run has
-  static constexpr int OVERHEAD = 32, LEAST = 24;
+  // what a segment costs besides its blocks, in blocks (16 / 32 / 64: trees of
+  // 24 over 8 contexts of 4099 85 / 76 / 84 us, trees of 32 over 16 of up to
+  // 2000 88 / 85 / 99), and the least a run has
+  static constexpr int OVERHEAD = 32, LEAST = 12;
 };
 
 // The barriers of a thread block.

@@ -98,8 +98,9 @@ struct KvAttentionPlan {
   int nt, grid;
   int64_t slot_floats, part_bytes;
 };
-// grid 0: the format is not built.
-KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows);
+// blocks: as many as the batch's sequences may have, of all heads.  grid 0: the
+// format is not built.
+KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows, int64_t blocks);
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, int hd, int bits, int group,
                                 const KvAttentionPlan& plan, cudaStream_t stream);
 

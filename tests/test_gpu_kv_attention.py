@@ -357,6 +357,7 @@ def test_more_new_rows_than_a_mask_holds_are_refused():
 
 
 WIDE = [(hd, b, g) for hd, b, g in FORMATS if hd <= 128 and hd // g <= 2]
+ROOM = 9000     # columns of the page table: those tiles are for batches that may be long
 
 
 @pytest.mark.parametrize("hd,bits,group", WIDE)
@@ -364,7 +365,8 @@ WIDE = [(hd, b, g) for hd, b, g in FORMATS if hd <= 128 and hd // g <= 2]
 def test_tiles_of_256_rows_of_every_format(hd, bits, group, tree):
     """Full, ragged and nearly empty tiles of rows; lengths around a step's 64 tokens."""
     new = [64, 61, 0, 3, 64]
-    case = R.Case(new, [64, 127, 20, 67, 200], heads=1, hd=hd, bits=bits, group=group, page=32, seed=hd + bits + group)
+    case = R.Case(new, [64, 127, 20, 67, 200], heads=1, hd=hd, bits=bits, group=group, page=32, seed=hd + bits + group,
+                  table_extra=ROOM)
     check(case, per=4, masks=_trees(new, 5) if tree else None)
 
 
@@ -377,14 +379,14 @@ def test_tiles_of_256_rows(kw):
     per = kw.pop("per", 4)
     small = kw.pop("small", False)
     case = R.Case(new, [300, 64, 131], heads=2, hd=128, bits=4, group=64, page=16, seed=31, stat=kw.pop("stat", False),
-                  scheme=kw.pop("scheme", None), extra_rows=kw.pop("rows", 0),
+                  scheme=kw.pop("scheme", None), extra_rows=kw.pop("rows", 0), table_extra=ROOM,
                   scale_of=(lambda which, b: 1e-3 * 40.0 ** b) if small else (lambda which, b: 1.0))
     check(case, per=per, masks=_trees(new, 6), **kw)
 
 
 def test_wide_tiles_of_long_contexts_are_cut_and_joined():
     """Enough steps that a segment's parts are many, their maxima apart; every time the same bits."""
-    case = R.Case([64], [7000], heads=1, hd=64, bits=4, group=64, page=64, seed=32)
+    case = R.Case([64], [7000], heads=1, hd=64, bits=4, group=64, page=64, seed=32, table_extra=ROOM)
     Q = (torch.randn(64, 4, 64, generator=torch.Generator().manual_seed(33)) * 3).to(bf16)
     Y = check(case, per=4, Q=Q)
     for _ in range(3):
@@ -393,7 +395,7 @@ def test_wide_tiles_of_long_contexts_are_cut_and_joined():
 
 def test_wide_tiles_skip_what_is_not_there():
     """NaN scales in sight of some rows, pages that are not the cache's, sequences that are not valid."""
-    case = R.Case([64, 64], [150, 100], heads=1, hd=128, bits=4, group=128, page=16, seed=34)
+    case = R.Case([64, 64], [150, 100], heads=1, hd=128, bits=4, group=128, page=16, seed=34, table_extra=ROOM)
     masks = [1 << i for i in range(64)] * 2       # every new token sees the old ones and itself
     cache, batch = case.on_gpu()
     Q = torch.randn(128, 4, 128, generator=torch.Generator().manual_seed(35)).to(bf16).cuda()

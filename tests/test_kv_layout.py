@@ -57,6 +57,14 @@ def _batch(B=3, T=5, max_new=2):
     return ttq.KVBatch(torch.zeros((B, 2), dtype=i32), torch.zeros(B, dtype=i32), torch.zeros(B + 1, dtype=i32), T, max_new)
 
 
+@pytest.mark.parametrize("hd,bits,group", FORMATS)
+def test_a_workspace_serves_fewer_rows_too(hd, bits, group):
+    """Whatever tile a batch of fewer new rows takes."""
+    for per in (1, 3, 4, 5, 8, 33):
+        sizes = [ttq.ttq_kv_attention_workspace_size(hd, bits, group, 2 * per, 2, n) for n in range(65)]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+
+
 def test_handles_check_their_tensors():
     n = ttq.ttq_kv_page_bytes(32, 2, 128, 4, 64)
     with pytest.raises(ValueError, match="pages must be"):
