@@ -5,7 +5,8 @@
 // with K_j = s (c - z) D_k^{-1/2} per group of channels, V_j likewise.
 //
 // Work.  The rows of one key/value head (its query heads x the sequence's
-// new tokens) form tiles of 8 NT rows; a segment is one (sequence, head,
+// new tokens) form tiles of 8 NT rows, or of 256 where there are many
+// (kv_attention_wide.cuh); a segment is one (sequence, head,
 // tile) with all blocks of 16 tokens that it may see.  All segments'
 // blocks, laid end to end, are cut into equal runs, one per thread block of
 // the grid, so that contexts of any lengths load the SMs evenly.  The warps
