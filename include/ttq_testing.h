@@ -3,7 +3,8 @@
  * interface (the method has no counterpart): they exist so that a test can
  * show that the library's bounded device waits really run out, report
  * TTQ_ERR_TIMEOUT through the workspace status word, and leave the CUDA
- * context usable.
+ * context usable, and that a page lookup which no test could reach by its
+ * size is right.
  */
 #ifndef TTQ_TESTING_H_
 #define TTQ_TESTING_H_
@@ -30,6 +31,12 @@ typedef enum ttq_testing_wait {
  * out of range. */
 ttq_status ttq_testing_wait_timeout(int kind, uint64_t limit_ns, int blocks, void* ws,
                                     size_t ws_bytes, void* stream);
+
+/* The page (index into a row of the page table) of a key/value cache's block
+ * of 16 positions, as the kernels find it: block / (page_size / 16).  Host
+ * only.  page_size as for ttq_kv_cache, block 0 to 2^27 - 1; -1 for
+ * arguments out of range. */
+int64_t ttq_testing_kv_page_of(int page_size, int64_t block);
 
 #ifdef __cplusplus
 }

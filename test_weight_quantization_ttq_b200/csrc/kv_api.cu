@@ -64,10 +64,9 @@ ttq_status geometry(const ttq_kv_cache* c, const ttq_kv_batch* b, void* ws, size
   g->pages = static_cast<uint8_t*>(c->pages);
   g->num_pages = c->num_pages;
   g->page_bytes = static_cast<int64_t>(page_bytes(c->page_size, c->kv_heads, c->head_dim, c->bits, c->group));
-  g->page_blocks = c->page_size / 16;
+  g->set_page_blocks(c->page_size / 16);
   g->kv_heads = c->kv_heads;
   g->table = b->page_table;
-  g->page_magic = ((1ull << 40) + g->page_blocks - 1) / g->page_blocks;
   g->table_stride = b->table_stride;
   g->kv_len = b->kv_len;
   g->cu = b->cu_new;

@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
       const int j = i + lane, blk = blk0 + j;
       src = nullptr;
       if (j < count) {
-        const int pg = static_cast<int>(static_cast<uint64_t>(blk) * a.g.page_magic >> 40);   // blk / page_blocks
+        const int pg = g.page_of(blk);
         const int page = g.table[seg.b * g.table_stride + pg];
         if (page >= 0 && page < g.num_pages)
           src = g.pages + page * g.page_bytes +

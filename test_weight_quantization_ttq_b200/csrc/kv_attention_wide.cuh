@@ -174,8 +174,7 @@ struct KvWidePart {
   // when its block is due
   __device__ __forceinline__ int page_of(int j) const {
     if (j >= count) return -1;
-    const int pg = static_cast<int>(static_cast<uint64_t>(blk0 + j) * a.g.page_magic >> 40);
-    return __ldg(a.g.table + b * a.g.table_stride + pg);
+    return __ldg(a.g.table + b * a.g.table_stride + a.g.page_of(blk0 + j));
   }
   __device__ __forceinline__ void load(int j, int page, int which, Raw& x) const {
     const int lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
@@ -188,7 +187,7 @@ struct KvWidePart {
       if (j < count && lane == 0) set_flag(a.g.status, TTQ_FLAG_BAD_INDEX);
       return;
     }
-    const int blk = blk0 + j, pg = static_cast<int>(static_cast<uint64_t>(blk) * a.g.page_magic >> 40);
+    const int blk = blk0 + j, pg = a.g.page_of(blk);
     const uint8_t* part = a.g.pages + page * a.g.page_bytes +
                           (static_cast<int64_t>(h) * a.g.page_blocks + (blk - pg * a.g.page_blocks)) * F::BLOCK + which * F::V_OFFSET;
 #pragma unroll

@@ -43,10 +43,8 @@ inline cudaError_t kv_allow_smem(const void* kernel, int bytes, std::atomic<uint
 struct KvGeometry {
   uint8_t* pages = nullptr;
   int64_t num_pages = 0, page_bytes = 0;
-  int page_blocks = 1;          // blocks of 16 tokens in a page
-  // ceil(2^40 / page_blocks): n * page_magic >> 40 is n / page_blocks for n < 2^28
-  // and page_blocks <= 4096 (the product is off by less than n 4096 < 2^40)
-  uint64_t page_magic = 0;
+  int page_blocks = 1;          // blocks of 16 tokens in a page, 1 to 4096
+  uint32_t page_magic = 1u << 27, page_shift = 0;   // of page_of
   int kv_heads = 1;
   const int32_t* table = nullptr;
   int64_t table_stride = 0;
@@ -56,6 +54,23 @@ struct KvGeometry {
   int64_t rows = 0;
   int max_new = 0;
   uint32_t* status = nullptr;
+
+  void set_page_blocks(int n) {
+    page_blocks = n;
+    page_shift = 0;
+    while ((1 << page_shift) < n) ++page_shift;
+    page_magic = static_cast<uint32_t>(((1ull << (27 + page_shift)) + n - 1) / n);
+  }
+  // blk / page_blocks for every block of 2^31 positions, 0 <= blk < 2^27: with
+  // d = page_blocks <= 2^k, k = page_shift, the magic number is less than one
+  // above 2^(27 + k) / d, so blk times it is less than 2^27 <= 2^(27 + k) / d
+  // above 2^(27 + k) blk / d, too little to reach the next whole quotient.
+  // (The magic number is at most 2^28, the shifted block below 2^32: a
+  // multiplication's high word and a shift.)
+  __host__ __device__ __forceinline__ int page_of(int blk) const {
+    const uint32_t n = static_cast<uint32_t>(blk) << 5;
+    return static_cast<int>(static_cast<uint32_t>(static_cast<uint64_t>(n) * page_magic >> 32) >> page_shift);
+  }
 };
 
 struct KvWriteArgs {

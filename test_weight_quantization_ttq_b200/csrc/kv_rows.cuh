@@ -124,7 +124,7 @@ struct KvWalk {
     }
     const int4 s = seqs[b];
     const int old = s.y - s.w, blk = (old >> 4) + ordinal - (b > 0 ? seqs[b - 1].x : 0);
-    const int pg = static_cast<int>(static_cast<uint64_t>(blk) * g.page_magic >> 40);   // blk / page_blocks
+    const int pg = g.page_of(blk);
     KvTask k;
     k.page = __ldg(g.table + b * g.table_stride + pg);
     k.at = blk - pg * g.page_blocks;

@@ -1,6 +1,7 @@
-// Test hooks (include/ttq_testing.h): waits that cannot complete, made with
+// Test hooks (include/ttq_testing.h).  Waits that cannot complete, made with
 // the kernels' own bounded wait routines and a short limit, so that a test
 // can see the timeout path end in TTQ_FLAG_TIMEOUT and a usable context.
+#include "kv_kernels.h"
 #include "ttq_device.cuh"
 #include "ttq_kernels.h"
 #include "ttq_testing.h"
@@ -34,4 +35,11 @@ extern "C" ttq_status ttq_testing_wait_timeout(int kind, uint64_t limit_ns, int 
                                            static_cast<cudaStream_t>(stream), false, limit_ns,
                                            static_cast<uint32_t*>(ws));
   return e == cudaSuccess ? TTQ_OK : TTQ_ERR_CUDA;
+}
+
+extern "C" int64_t ttq_testing_kv_page_of(int page_size, int64_t block) {
+  if (page_size < 16 || page_size > 65536 || page_size % 16 != 0 || block < 0 || block >= (1 << 27)) return -1;
+  ttq::KvGeometry g;
+  g.set_page_blocks(page_size / 16);
+  return g.page_of(static_cast<int>(block));
 }

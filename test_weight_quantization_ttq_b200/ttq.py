@@ -91,6 +91,7 @@ SIGNATURES = {
     "ttq_linear_forward_kernels": (_INT, [_INT, _I64, _I64, _I64, _I64, _F, _INT, _INT, _INT,
                                           ctypes.POINTER(ctypes.c_int)]),
     "ttq_testing_wait_timeout": (_INT, [_INT, ctypes.c_uint64, _INT, _P, _SZ, _P]),
+    "ttq_testing_kv_page_of": (_I64, [_INT, _I64]),
     "ttq_quantize_gemm": (_INT, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _INT, _INT, _P, _P, _P,
                                  _P, _INT, _P, _SZ, _P]),
     "ttq_get_status": (_INT, [_P, ctypes.POINTER(ctypes.c_uint32)]),
@@ -527,6 +528,12 @@ def ttq_testing_wait_timeout(kind, limit_ns, blocks, ws, stream=None) -> None:
     complete, with a limit of limit_ns; they set TTQ_FLAG_TIMEOUT in ws."""
     _check(lib().ttq_testing_wait_timeout(kind, limit_ns, blocks, _dev(ws, "ws"), _nbytes(ws),
                                           _stream(stream)), "ttq_testing_wait_timeout")
+
+
+def ttq_testing_kv_page_of(page_size, block) -> int:
+    """Test hook (host only): the page, counted along its sequence, of a block of 16 positions, as the cache's kernels
+    find it; -1 for arguments out of range."""
+    return int(lib().ttq_testing_kv_page_of(page_size, block))
 
 
 def ttq_quantize_gemm(W, D, Xs, A, B, X, bits, group, ws=None, Y=None, y_dtype=torch.bfloat16,
