@@ -155,13 +155,19 @@ cudaError_t launch_kv_read(const KvReadArgs& a, int hd, int bits, int group, int
   const dim3 grid(part_grid(a.g, num_sms, hd == 256 || dtype == kRowF32 ? 2 : 3));
   with_format(hd, bits, group, [&](auto HDc, auto BITSc, auto NGc) {
     constexpr int HD = decltype(HDc)::value, BITS = decltype(BITSc)::value, NG = decltype(NGc)::value;
-    auto* k = dtype == kRowF32    ? kv_read_kernel<HD, BITS, NG, kRowF32>
-              : dtype == kRowBF16 ? kv_read_kernel<HD, BITS, NG, kRowBF16>
-                                  : kv_read_kernel<HD, BITS, NG, kRowF16>;
-    const int smem = kWarps * 16 * (HD * (dtype == kRowF32 ? 4 : 2) + 16) + 16 * a.g.batch;
-    // above 48 KiB (float32 rows, heads of 256, the largest batches) a kernel needs leave
-    if (smem > 48 * 1024 && (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return;
-    e = launch_kernel(k, grid, dim3(kThreads), smem, stream, true, a);
+    auto go = [&](auto TYPEc) {
+      constexpr int TYPE = decltype(TYPEc)::value;
+      constexpr int bytes = kWarps * 16 * (HD * (TYPE == kRowF32 ? 4 : 2) + 16);
+      auto* k = kv_read_kernel<HD, BITS, NG, TYPE>;
+      // the leave is for the largest batch, whatever this call's is: another
+      // thread may be between it and its launch
+      static std::atomic<uint64_t> set{0};
+      if ((e = kv_allow_smem(reinterpret_cast<const void*>(k), bytes + 16 * kKvMaxBatch, set)) != cudaSuccess) return;
+      e = launch_kernel(k, grid, dim3(kThreads), bytes + 16 * a.g.batch, stream, true, a);
+    };
+    if (dtype == kRowF32) go(std::integral_constant<int, kRowF32>{});
+    else if (dtype == kRowBF16) go(std::integral_constant<int, kRowBF16>{});
+    else go(std::integral_constant<int, kRowF16>{});
   });
   return e;
 }
