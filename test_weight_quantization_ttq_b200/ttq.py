@@ -722,61 +722,82 @@ def _empty_rows(rows, heads, head_dim, dtype, device, stream) -> torch.Tensor:
     return _empty((rows, heads, head_dim), dtype, device, stream)
 
 
-class KVCache:
+class _Handle:
+    """A C struct built from the public attributes at the first call, after checking them, and again after one of them
+    was assigned."""
+    _struct = None
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if not name.startswith("_"):
+            object.__setattr__(self, "_struct", None)
+
+    def _keep(self, struct, device):
+        self._ref, self._device = ctypes.byref(struct), device
+        self._struct = struct     # last: another thread takes the struct for built from here on
+
+
+class KVCache(_Handle):
     """A quantised key/value cache (ttq_kv_cache): `pages` uint8 [num_pages][ttq_kv_page_bytes(...)] (new_kv_cache
     makes it) and its format; D_k, D_v and their inverse square roots float32 [kv_heads][head_dim] or None, as
-    ttq_act_norm gives them for rows of K and V.  It keeps the tensors; replacing one takes a new KVCache."""
+    ttq_act_norm gives them for rows of K and V.  It keeps the tensors; attributes may be assigned, and count from the
+    next call on."""
 
     def __init__(self, pages, page_size, kv_heads, head_dim, bits, group, scheme=TTQ_QSCHEME_ASYMMETRIC, D_k=None,
                  D_v=None, D_k_rsqrt=None, D_v_rsqrt=None):
-        n = ttq_kv_page_bytes(page_size, kv_heads, head_dim, bits, group)
-        if pages.dtype != torch.uint8 or pages.dim() != 2 or pages.shape[1] != n:
-            raise ValueError(f"pages must be uint8 [num_pages][{n}], got {pages.dtype} {tuple(pages.shape)}")
-        for t, name in ((D_k, "D_k"), (D_v, "D_v"), (D_k_rsqrt, "D_k_rsqrt"), (D_v_rsqrt, "D_v_rsqrt")):
-            _vector(t, name, kv_heads * head_dim)
-        for a, b, name in ((D_k, D_k_rsqrt, "k"), (D_v, D_v_rsqrt, "v")):
-            if (a is None) != (b is None):
-                raise ValueError(f"D_{name} and D_{name}_rsqrt are given together or not at all")
         self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, kv_heads, head_dim
         self.bits, self.group, self.scheme = bits, group, scheme
         self.D_k, self.D_v, self.D_k_rsqrt, self.D_v_rsqrt = D_k, D_v, D_k_rsqrt, D_v_rsqrt
-        self._struct = None
+        self._check()
+
+    def _check(self):
+        pages, n = self.pages, ttq_kv_page_bytes(self.page_size, self.kv_heads, self.head_dim, self.bits, self.group)
+        if pages.dtype != torch.uint8 or pages.dim() != 2 or pages.shape[1] != n:
+            raise ValueError(f"pages must be uint8 [num_pages][{n}], got {pages.dtype} {tuple(pages.shape)}")
+        for name in ("D_k", "D_v", "D_k_rsqrt", "D_v_rsqrt"):
+            _vector(getattr(self, name), name, self.kv_heads * self.head_dim)
+        for a, b, name in ((self.D_k, self.D_k_rsqrt, "k"), (self.D_v, self.D_v_rsqrt, "v")):
+            if (a is None) != (b is None):
+                raise ValueError(f"D_{name} and D_{name}_rsqrt are given together or not at all")
 
     def _arg(self):
         """(the C struct, its device), which is the current one."""
         if self._struct is None:
-            self._struct = _CacheStruct(_dev(self.pages, "pages"), self.pages.shape[0], self.page_size, self.kv_heads,
-                                        self.head_dim, self.bits, self.group, self.scheme, _dev(self.D_k, "D_k"),
-                                        _dev(self.D_v, "D_v"), _dev(self.D_k_rsqrt, "D_k_rsqrt"),
-                                        _dev(self.D_v_rsqrt, "D_v_rsqrt"))
-            self._ref, self._device = ctypes.byref(self._struct), self.pages.get_device()
+            self._check()
+            self._keep(_CacheStruct(_dev(self.pages, "pages"), self.pages.shape[0], self.page_size, self.kv_heads,
+                                    self.head_dim, self.bits, self.group, self.scheme, _dev(self.D_k, "D_k"),
+                                    _dev(self.D_v, "D_v"), _dev(self.D_k_rsqrt, "D_k_rsqrt"),
+                                    _dev(self.D_v_rsqrt, "D_v_rsqrt")), self.pages.get_device())
         elif self._device != torch.cuda.current_device():
             raise ValueError(f"pages is on {self.pages.device}; the library runs on the current device "
                              f"cuda:{torch.cuda.current_device()}")
         return self._ref, self._device
 
 
-class KVBatch:
+class KVBatch(_Handle):
     """The rows of a call (ttq_kv_batch): sequence i has rows cu_new[i] .. cu_new[i + 1] - 1, its last positions of
     kv_len[i]; page_table int32 [batch][pages], kv_len int32 [batch], cu_new int32 [batch + 1] (device tensors whose
-    contents may change between calls), `rows` rows in the row tensors, at most max_new of any sequence."""
+    contents may change between calls), `rows` rows in the row tensors, at most max_new of any sequence.  Attributes
+    may be assigned, and count from the next call on."""
 
     def __init__(self, page_table, kv_len, cu_new, rows, max_new):
-        _ints(kv_len, "kv_len", (None,))
-        n = kv_len.shape[0]
-        _ints(cu_new, "cu_new", (n + 1,))
-        _ints(page_table, "page_table", (n, None))
-        if rows < 0 or max_new < 0:
-            raise ValueError(f"rows and max_new must not be negative, got {rows} and {max_new}")
         self.page_table, self.kv_len, self.cu_new, self.rows, self.max_new = page_table, kv_len, cu_new, rows, max_new
-        self._struct = None
+        self._check()
+
+    def _check(self):
+        _ints(self.kv_len, "kv_len", (None,))
+        n = self.kv_len.shape[0]
+        _ints(self.cu_new, "cu_new", (n + 1,))
+        _ints(self.page_table, "page_table", (n, None))
+        if self.rows < 0 or self.max_new < 0:
+            raise ValueError(f"rows and max_new must not be negative, got {self.rows} and {self.max_new}")
 
     def _arg(self, device):
         if self._struct is None:
-            self._struct = _BatchStruct(_on(self.page_table, "page_table", device), self.page_table.shape[1],
-                                        _on(self.kv_len, "kv_len", device), _on(self.cu_new, "cu_new", device),
-                                        self.kv_len.shape[0], self.rows, self.max_new)
-            self._ref, self._device = ctypes.byref(self._struct), device
+            self._check()
+            self._keep(_BatchStruct(_on(self.page_table, "page_table", device), self.page_table.shape[1],
+                                    _on(self.kv_len, "kv_len", device), _on(self.cu_new, "cu_new", device),
+                                    self.kv_len.shape[0], self.rows, self.max_new), device)
         if self._device != device:
             raise ValueError(f"the batch is on {self.kv_len.device}, the cache on cuda:{device}")
         return self._ref
