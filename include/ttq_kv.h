@@ -133,7 +133,8 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
  *   - of the positions before the sequence's new ones, all;
  *   - of the new ones, without `tree` itself and the earlier ones, with
  *     `tree` (uint64 [rows], one mask per row) new token k iff bit k of its
- *     mask is set (its own bit included);
+ *     mask is set (its own bit included; bits at and above the number of the
+ *     sequence's rows stand for nothing);
  *   - with window > 0 only those less than `window` positions back, where a
  *     new token's position is the number of old ones plus the number of new
  *     ones that it sees besides itself (its depth in the tree).

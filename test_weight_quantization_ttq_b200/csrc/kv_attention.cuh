@@ -255,6 +255,12 @@ struct KvRuns {
   }
 };
 
+// Which of its sequence's n new tokens row i_new sees, as bits.  What a tree's
+// mask has beyond them stands for no token.
+__device__ __forceinline__ uint64_t kv_new_tokens(const KvAttentionArgs& a, int row0, int n, int i_new) {
+  return a.tree != nullptr ? a.tree[row0 + i_new] & ~0ull >> (64 - n) : (2ull << i_new) - 1ull;
+}
+
 // Which of block blk's 16 tokens a row sees (bit t): of the old tokens all, of
 // the new ones those of its mask, with a window those less than `window` back.
 __device__ __forceinline__ uint32_t kv_visible(const KvAttentionArgs& a, int row0, int old, int kv, int blk, uint64_t mask,
@@ -272,7 +278,7 @@ __device__ __forceinline__ uint32_t kv_visible(const KvAttentionArgs& a, int row
 #pragma unroll 1
       for (int j = max(j0, 0); j < there; ++j) {
         const int k_new = j - j0;
-        if (pos - old - __popcll(a.tree[row0 + k_new] & ~(1ull << k_new)) >= a.window) since &= ~(1u << j);
+        if (pos - old - __popcll(kv_new_tokens(a, row0, kv - old, k_new) & ~(1ull << k_new)) >= a.window) since &= ~(1u << j);
       }
     }
   }
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
         const int r = OWN * warp + lane, rr = min(r0 + r, R - 1), i_new = rr / a.per;
         const int64_t row = seg.row0 + i_new;
         q_at = row * a.q_row + (seg.h * a.per + rr - i_new * a.per) * a.q_head;
-        const uint64_t mask = a.tree != nullptr ? a.tree[row] : (2ull << i_new) - 1ull;
+        const uint64_t mask = kv_new_tokens(a, seg.row0, seg.n, i_new);
         row_mask[r] = mask;
         row_pos[r] = old + __popcll(mask & ~(1ull << i_new));
       }

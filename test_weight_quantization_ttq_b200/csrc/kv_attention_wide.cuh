@@ -119,7 +119,7 @@ struct KvWidePart {
     const int warp = tid >> 5, lane = tid & 31, R = n * a.per;
     if (tid < A::ROWS) {
       const int rr = min(r0 + tid, R - 1), i_new = rr / a.per;
-      const uint64_t mask = a.tree != nullptr ? a.tree[row0 + i_new] : (2ull << i_new) - 1ull;
+      const uint64_t mask = kv_new_tokens(a, row0, n, i_new);
       row_mask[tid] = mask;
       row_pos[tid] = old + __popcll(mask & ~(1ull << i_new));
     }

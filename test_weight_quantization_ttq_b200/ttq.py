@@ -882,7 +882,7 @@ def ttq_kv_attention(cache, batch, Q, scale, softcap=0.0, window=0, tree=None, w
                      stream=None):
     """Y [rows][heads][head_dim]: attention of the batch's rows of Q (strided like K of ttq_kv_write) over the cache,
     causal among a sequence's own rows, or by `tree` (int64 [rows]: bit k of a row's mask is set iff it sees the
-    sequence's k-th new row).  softcap: scores are softcap tanh(t / softcap); window: positions seen, 0 for all."""
+    sequence's k-th new row; bits beyond its rows stand for nothing).  softcap: scores are softcap tanh(t / softcap); window: positions seen, 0 for all."""
     q_strides = _rows_of(Q, "Q", batch.rows, None, cache.head_dim)
     heads = Q.shape[1]
     if heads % cache.kv_heads or heads == 0:
