@@ -145,8 +145,13 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
  * accumulation: each row of Q (times D_k_rsqrt), scaled by a power of two,
  * is rounded to binary16 (bf16 and binary16 rows lose nothing to it but
  * elements under 2^-14 of the row's largest), the codes less their zeros
- * are exact, the probabilities times V's scales are rounded to binary16.
- * Scores, maxima and sums are fp32.  Deterministic for given inputs.  ws:
+ * are exact, the probabilities times V's scales are rounded to binary16, in
+ * units in which the largest product of a probability and a scale that the
+ * row meets is near 1: products under 2^-14 of it are subnormal and keep
+ * 2^-25 of it.  (The unit goes by each token's largest scale; a group of
+ * channels whose scales lie 2^14 below another group's has only such
+ * products.)  What a row does not see has no effect on it.  Scores, their
+ * running maxima and sums are fp32.  Deterministic for given inputs.  ws:
  * ttq_kv_attention_workspace_size(...) bytes, initialised once by
  * ttq_workspace_init (every call leaves its counters at zero) and again
  * after TIMEOUT; calls that may run at the same time need one each.  Flags

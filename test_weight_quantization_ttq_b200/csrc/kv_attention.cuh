@@ -41,11 +41,15 @@
 // the B operand's by an 8 x 8 transposition within the warp.
 //
 // Numerics.  Each row of q (times D_k^{-1/2}) is scaled by a power of two to
-// [1, 2) and rounded to binary16.  Scores, the running maximum m and the sum
-// l are fp32.  m moves only when a score exceeds it by more than 8 (in
-// powers of two), which keeps p <= 256; p s_V is rounded to binary16 after
-// scaling by 2^-E, 2^E a scale of V that no scale so far exceeds more than 64
-// times, so that scales of any size use binary16's normal range.
+// [1, 2) and rounded to binary16.  Scores t (in powers of two), the row's
+// offset and the sum l are fp32.  What is rounded to binary16 is p s_V, so the
+// offset that p = 2^(t - offset) is taken off by is not the largest score but
+// the largest t + e of the tokens that the row sees, 2^e the power of two in
+// the token's largest scale of V (its groups share it): p s_V of the weightiest
+// token is near 1, whatever the scales are, and a token that the row does not
+// see, or that has no probability, takes no bits from the others.  The offset
+// moves only when a t + e exceeds it by more than 8, which keeps p s_V below
+// 2^9; products under 2^-14 are binary16's subnormal numbers.
 #pragma once
 
 #include <atomic>
@@ -57,8 +61,14 @@
 namespace ttq {
 
 constexpr float kKvLog2e = 1.4426950408889634f;
-constexpr float kKvFloor = -1e30f;    // running maximum before any score
+constexpr float kKvFloor = -3.4e38f;  // a row's offset before any score
 constexpr float kKvSlack = 8.f;
+constexpr float kKvLeastScale = 5.9604645e-08f;   // 2^-24, binary16's least: what a token without a scale counts for
+
+// The exponent of a positive float: the integer put under 2^23's exponent, which counts it.
+__device__ __forceinline__ float kv_exponent(float x) {
+  return __uint_as_float(__float_as_uint(x) >> 23 | 0x4B000000u) - 8388735.f;   // 2^23 + 127
+}
 
 template <int HD, int BITS, int NG, int NT>
 struct KvAttention {
@@ -629,12 +639,11 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
 
     // ---- the loop over this warp's blocks
     float o[MT][NT][4] = {};
-    float m[NT][2] = {}, l[NT][2] = {};
+    float off[NT][2] = {}, l[NT][2] = {};
     constexpr uint32_t ALL = (1u << (2 * NT)) - 1;
-    uint32_t seen = 0;                          // columns (bit 2 nt + c) whose maximum is a score's
+    uint32_t seen = 0;                          // columns (bit 2 nt + c) whose offset is a token's
     bool all_seen = false;                      // all columns of all lanes
-    float vf = 1.2676506e30f;                   // 2^-E; at first 2^100, so that any scale lowers it
-    float zs[A::VRAW ? NG : 1][4] = {};         // sums of p s (offset + z) 2^-E per group
+    float zs[A::VRAW ? NG : 1][4] = {};         // sums of p s (the fields' offset + z) per group
     int plain0, plain1;
     unmasked(blk0, count, plain0, plain1);
     const uint32_t q_frags = smem_addr(qfrag) + lane * 16;
@@ -740,7 +749,7 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
           for (int k = 0; k < NG; ++k) vz[r][k] = __byte_perm(e[k], e[NG + k], 0x7632);
         }
       }
-      // -- scores in powers of two less the running maximum
+      // -- scores in powers of two less the row's offset
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float2 f = *reinterpret_cast<const float2*>(q_factor + 8 * nt + 2 * tq);
@@ -748,11 +757,11 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float t = s[nt][i] * ((i & 1) ? f.y : f.x);
-            s[nt][i] = a.cap * kKvLog2e * (1.f - 2.f * kv_rcp(1.f + kv_exp2(t * (2.f * kKvLog2e)))) - m[nt][i & 1];
+            s[nt][i] = a.cap * kKvLog2e * (1.f - 2.f * kv_rcp(1.f + kv_exp2(t * (2.f * kKvLog2e)))) - off[nt][i & 1];
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] = fmaf(s[nt][i], (i & 1) ? f.y : f.x, -m[nt][i & 1]);
+          for (int i = 0; i < 4; ++i) s[nt][i] = fmaf(s[nt][i], (i & 1) ? f.y : f.x, -off[nt][i & 1]);
         }
       }
       // -- masks: lane r finds which of the block's tokens row r sees; tokens
@@ -780,41 +789,34 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
           }
         }
       }
-      float top = 0.f, most = s[0][0];          // the largest scale and score (NaN aside)
+      // -- the offsets move only when a t + e is well above one (and to a
+      // column's first); whether one may is asked of the lane's largest score
+      // and scale (NaN aside) first
+      float top[2] = {kKvLeastScale, kKvLeastScale}, most = s[0][0];
 #pragma unroll
-      for (int k = 0; k < NG; ++k) top = fmaxf(top, fmaxf(vs[0][k], vs[1][k]));
+      for (int k = 0; k < NG; ++k) top[0] = fmaxf(top[0], vs[0][k]), top[1] = fmaxf(top[1], vs[1][k]);
 #pragma unroll
       for (int i = 1; i < 4 * NT; ++i) most = fmaxf(most, s[i / 4][i % 4]);
-      // -- the running maxima move only when one is well above them (and to a
-      // column's first score)
-      if (__any_sync(0xffffffffu, !all_seen || top * vf > 64.f || most > kKvSlack)) {
-        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-        float fv = 1.f;
-        if (top * vf > 64.f) {
-          // 2^-e for a scale in [2^e, 2^(e + 1)): its exponent's complement
-          const float vf_new = __uint_as_float((254u - (__float_as_uint(top) >> 23)) << 23);
-          fv = vf_new / vf;
-          vf = vf_new;
-        }
+      if (__any_sync(0xffffffffu, !all_seen || most + kv_exponent(fmaxf(top[0], top[1])) > kKvSlack)) {
+        const float e0 = kv_exponent(top[0]), e1 = kv_exponent(top[1]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float up = fmaxf(s[nt][c], s[nt][c + 2]);
+            float up = fmaxf(s[nt][c] + e0, s[nt][c + 2] + e1);
             up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 4));
             up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 8));
             up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
             const uint32_t bit = 1u << (2 * nt + c);
-            // (each column by its own scores, so that no row's result depends on another's)
+            // (each column by its own tokens, so that no row's result depends on another's)
             if (!(up > -INFINITY) || ((seen & bit) && up <= kKvSlack)) up = 0.f;
             else seen |= bit;
             // (before the first score l and o are zero, or NaN)
-            float f = up < 0.f ? 1.f : kv_exp2(-up);
-            m[nt][c] += up;
+            const float f = up < 0.f ? 1.f : kv_exp2(-up);
+            off[nt][c] += up;
             s[nt][c] -= up;
             s[nt][c + 2] -= up;
             l[nt][c] *= f;
-            f *= fv;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               o[mt][nt][c] *= f;
@@ -837,17 +839,16 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
           s[nt][i] = kv_exp2(s[nt][i]);
           l[nt][i & 1] += s[nt][i];
         }
-      // -- p s_V 2^-E as the B operand, and the second product
+      // -- p s_V as the B operand, and the second product
       constexpr int MTG = MT / NG;              // m tiles of a group
       constexpr int MTW = BITS == 8 ? 1 : 16 / BITS / 2;   // m tiles of a word
       uint32_t vw[2][PW], pv[2][BITS == 8 ? 2 : 16 / BITS];
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
-        const float s0 = vs[0][k] * vf, s1 = vs[1][k] * vf;
         uint32_t b[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float w0 = s[nt][0] * s0, w1 = s[nt][1] * s0, w2 = s[nt][2] * s1, w3 = s[nt][3] * s1;
+          float w0 = s[nt][0] * vs[0][k], w1 = s[nt][1] * vs[0][k], w2 = s[nt][2] * vs[1][k], w3 = s[nt][3] * vs[1][k];
           if (masked) {                         // a NaN scale reaches only those that see its token
             kv_zero_with(w0, s[nt][0]);
             kv_zero_with(w1, s[nt][1]);
@@ -923,7 +924,6 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
     // accumulators go to their regions, the rows' results from there to Y or,
     // of a part, to the workspace
     {
-      const float back = 1.f / vf;
       float* tile = reinterpret_cast<float*>(ring);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -936,14 +936,14 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
           v += __shfl_xor_sync(0xffffffffu, v, 16);
           if (gr == 0) {
             warp_l[warp][r] = v;
-            warp_m[warp][r] = (seen >> (2 * nt + c) & 1u) ? m[nt][c] : kKvFloor;
+            warp_m[warp][r] = (seen >> (2 * nt + c) & 1u) ? off[nt][c] : kKvFloor;
           }
 #pragma unroll
           for (int mt = 0; mt < MT; mt += 2) {
             // the four channels of m tiles mt and mt + 1 that this lane holds of the row
             const int ch = 2 * mt / (F::G / 8) * F::G + gr * (F::G / 8) + 2 * mt % (F::G / 8);
             *reinterpret_cast<float4*>(tile + r * A::LDO + ch) =
-                make_float4(o[mt][nt][c] * back, o[mt][nt][c + 2] * back, o[mt + 1][nt][c] * back, o[mt + 1][nt][c + 2] * back);
+                make_float4(o[mt][nt][c], o[mt][nt][c + 2], o[mt + 1][nt][c], o[mt + 1][nt][c + 2]);
           }
         }
     }

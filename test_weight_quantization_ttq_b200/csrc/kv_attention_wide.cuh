@@ -17,11 +17,11 @@
 //     O_k += P_k V_k, all in tensor memory;
 //   8 (a thread a row) take S_k from tensor memory, s_K and the group sum,
 //     cap, masks and exponentials, and put P_k = p s_V as binary16 into
-//     shared memory.  O moves with the maximum there (rarely: see kKvSlack).
+//     shared memory.  O moves with the rows' offsets there (rarely: see
+//     kKvSlack).
 // The operands are in two buffers, and S too where tensor memory holds it
 // (one group), so that the next step's scores and unpacking overlap this
-// one's softmax.  p is scaled by 2^-E as well, l with it, so that E is part
-// of the maximum.
+// one's softmax.
 // Measured: trees of 64 over 16384 positions of E4M3, cap, 256 rows: 138 us
 // (8 tiles of 32: 165); trees of 24, 192 rows: 76 us (83).  Bound by the
 // latency of the softmax's steps, not by a pipe (the tensor pipe is 11% busy):
@@ -344,9 +344,8 @@ struct KvWidePart {
     const uint32_t lanes = static_cast<uint32_t>(r7 & ~31) << 16;
     const uint32_t o = tmem + lanes + A::O_AT + tile * HD;
     const float f = q_factor[r];
-    // scores in powers of two less off = m + E, 2^E as kv_attention.cuh has it
-    float m = 0.f, E = 0.f, l = 0.f;
-    bool seen = false, scaled = false;          // whether m and E are of a score and a scale
+    float off = 0.f, l = 0.f;                   // the row's offset and sum as kv_attention.cuh has them
+    bool seen = false;                          // whether the offset is a token's
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       const int T = turn0 + i, s = T & 1, sb = T % A::SB;
@@ -375,7 +374,6 @@ struct KvWidePart {
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.s_free[sb]);
       // -- scores
-      const float off = m + E;
       if (a.cap > 0.f) {      // cap tanh(t) = cap (1 - 2 / (1 + e^{2 t}))
 #pragma unroll
         for (int j = 0; j < N; ++j)
@@ -399,8 +397,10 @@ struct KvWidePart {
         for (int j = 0; j < N; ++j)
           if (!(half[j / 32] >> (j % 32) & 1u)) t[j] = -INFINITY;
       }
-      // -- the running maximum and E move only when one is well above them
-      float most[4] = {t[0], t[1], t[2], t[3]}, top = 0.f;
+      // -- the offset moves only when a t + e is well above it (and to the
+      // first); whether one may is asked of the largest score and scale (NaN
+      // aside) first
+      float most[4] = {t[0], t[1], t[2], t[3]}, top = kKvLeastScale;
 #pragma unroll
       for (int j = 4; j < N; ++j) most[j % 4] = fmaxf(most[j % 4], t[j]);
       const float high = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
@@ -408,18 +408,24 @@ struct KvWidePart {
       for (int k = 0; k < NG; ++k)
         top = fmaxf(top, fmaxf(s_v[(s * NG + k) * A::STEP + lane], s_v[(s * NG + k) * A::STEP + 32 + lane]));
       top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-      const bool lift = scaled ? top * kv_exp2(-E) > 64.f : top > 0.f;   // (E is an integer: exact)
-      const bool move = seen ? high + E > kKvSlack : high > -INFINITY;
+      const bool move = !seen || high + kv_exponent(top) > kKvSlack;
       if (T > 0 && !wait(&bars.pv_done, T - 1)) return;   // O is at rest, P is free
-      if (__any_sync(0xffffffffu, move || lift)) {
-        if (move) m += high + E;
-        if (lift) E = static_cast<float>(static_cast<int>(__float_as_uint(top) >> 23) - 127), scaled = true;
-        const float delta = (m + E) - off;
-        const float g = seen ? kv_exp2(-delta) : 1.f;
-        seen = seen || move;
+      if (__any_sync(0xffffffffu, move)) {
+        float up = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          float sc = kKvLeastScale;
+#pragma unroll
+          for (int k = 0; k < NG; ++k) sc = fmaxf(sc, s_v[(s * NG + k) * A::STEP + j]);
+          up = fmaxf(up, t[j] + kv_exponent(sc));
+        }
+        if (!(up > -INFINITY) || (seen && up <= kKvSlack)) up = 0.f;   // (a row by its own tokens)
+        const float g = seen ? kv_exp2(-up) : 1.f;   // (before the first token l and O are zero, or NaN)
+        seen = seen || high > -INFINITY;
+        off += up;
         l *= g;
 #pragma unroll
-        for (int j = 0; j < N; ++j) t[j] -= delta;
+        for (int j = 0; j < N; ++j) t[j] -= up;
         if (i > 0) {
           tc_fence_after_sync();
 #pragma unroll 1
@@ -465,7 +471,7 @@ struct KvWidePart {
     }
     if (!wait(&bars.pv_done, turn0 + steps - 1)) return;   // all products of the part are done
     tc_fence_after_sync();
-    *m_out = seen ? m + E : kKvFloor;
+    *m_out = seen ? off : kKvFloor;
     *l_out = l;
     float* to = reinterpret_cast<float*>(region) + r * A::LDO;
 #pragma unroll
