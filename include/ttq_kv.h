@@ -151,7 +151,9 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
  * 2^-25 of it.  (The unit goes by each token's largest scale; a group of
  * channels whose scales lie 2^14 below another group's has only such
  * products.)  What a row does not see has no effect on it.  Scores, their
- * running maxima and sums are fp32.  Deterministic for given inputs.  ws:
+ * running maxima and sums are fp32; a capped score is off by 2^-22 of the cap
+ * where that is at most 256, else by 2^-19 of itself, and a cap of 2^64 or
+ * more, which changes no fp32 score, is left out.  Deterministic for given inputs.  ws:
  * ttq_kv_attention_workspace_size(...) bytes, initialised once by
  * ttq_workspace_init (every call leaves its counters at zero) and again
  * after TIMEOUT; calls that may run at the same time need one each.  Flags

@@ -88,6 +88,11 @@ ttq_status status_of(cudaError_t e) { return e == cudaSuccess ? TTQ_OK : TTQ_ERR
 
 }  // namespace
 
+// cap tanh(t / cap) is t but for (t / cap)^2 / 3 of it, and at most cap: with a
+// cap of 2^64 all t to 2^52 are what they were, under 2^-64 all are zero beside 1.
+// (Between them 1 / cap, 2 / cap and cap log2(e) are normal numbers.)
+constexpr float kKvMostCap = 18446744073709551616.f, kKvLeastCap = 1.f / kKvMostCap;
+
 // Tiles of 256 rows pay where there is work for them: the blocks that the
 // batch's sequences may have, by the width of its page table (32 heads over 8,
 // trees of 48: 4000 blocks 54 us, 42 in tiles of 32; 8000 blocks 69 and 66;
@@ -220,7 +225,8 @@ ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch
   a.heads = static_cast<int>(heads);
   a.per = per;
   a.scale = scale;
-  a.cap = softcap;
+  // beyond these a cap changes no score in fp32, and makes all the same
+  a.cap = softcap >= kKvMostCap ? 0.f : softcap > 0.f && softcap < kKvLeastCap ? kKvLeastCap : softcap;
   a.window = window;
   a.tree = tree;
   a.Y = Y;

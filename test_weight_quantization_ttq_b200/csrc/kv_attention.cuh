@@ -144,6 +144,27 @@ __device__ __forceinline__ float kv_rcp(float x) {
   return r;
 }
 
+// cap tanh(x) in powers of two: cap (1 - 2 / (1 + e^{2 x})).  That is off by some
+// 2^-22 of the cap: `fine`, for caps of which that is too much for a score,
+// takes tanh of less than 1 / 4 from its series up to x^9 (the next term is
+// under 2^-26 of it), so that the score is off by 2^-19 of itself at most.
+constexpr float kKvFineCap = 256.f;   // 2^-22 of it moves a probability by 2^-14, an eighth of its rounding
+__device__ __forceinline__ float kv_cap(float x, float cap, bool fine) {
+  float y = 1.f - 2.f * kv_rcp(1.f + kv_exp2(x * (2.f * kKvLog2e)));
+  if (fine) {
+    const float u = x * x;
+    const float z = fmaf(u, fmaf(u, fmaf(u, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f);
+    y = fabsf(x) < 0.25f ? fmaf(x * u, z, x) : y;
+  }
+  return cap * kKvLog2e * y;
+}
+
+// t = sum * what this gives, or tanh's argument: the row's power of two and the
+// call's factor.  Held finite, so that a score of zero stays one.
+__device__ __forceinline__ float kv_row_factor(float factor, int exponent) {
+  return fminf(fmaxf(factor * __uint_as_float(static_cast<uint32_t>(exponent) << 23), -3.4e38f), 3.4e38f);
+}
+
 // w = 0 where p = 0.  (Left to the compiler, what few blocks need becomes a
 // select for all of them.)
 __device__ __forceinline__ void kv_zero_with(float& w, float p) {
@@ -610,7 +631,7 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
           qfrag[(((r >> 3) * (KS / 2) + idx / 8) * 32 + 4 * (r & 7) + quarter) * 4 + (idx % 8) / 2] =
               h2_as_u32(__floats2half2_rn(v[e] * down, v[e + 1] * down));
         }
-        if (lane == 0) q_factor[r] = factor * __uint_as_float(static_cast<uint32_t>(ex) << 23);
+        if (lane == 0) q_factor[r] = kv_row_factor(factor, ex);
       }
     }
     __syncthreads();
@@ -753,12 +774,10 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float2 f = *reinterpret_cast<const float2*>(q_factor + 8 * nt + 2 * tq);
-        if (a.cap > 0.f) {    // cap tanh(t) = cap (1 - 2 / (1 + e^{2 t}))
+        if (a.cap > 0.f) {
+          const bool fine = a.cap > kKvFineCap;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float t = s[nt][i] * ((i & 1) ? f.y : f.x);
-            s[nt][i] = a.cap * kKvLog2e * (1.f - 2.f * kv_rcp(1.f + kv_exp2(t * (2.f * kKvLog2e)))) - off[nt][i & 1];
-          }
+          for (int i = 0; i < 4; ++i) s[nt][i] = kv_cap(s[nt][i] * ((i & 1) ? f.y : f.x), a.cap, fine) - off[nt][i & 1];
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[nt][i] = fmaf(s[nt][i], (i & 1) ? f.y : f.x, -off[nt][i & 1]);

@@ -159,7 +159,7 @@ struct KvWidePart {
         const uint32_t at = smem_addr(region) + r / 128 * A::QB + c / 64 * (128 * 128) + r % 128 * 128 + (((c % 64 / 8) ^ (r & 7)) << 4) + c % 8 * 2;
 #pragma unroll
         for (int e = 0; e < E; e += 2) kv_sts32(at + 2 * e, h2_as_u32(__floats2half2_rn(v[e] * down, v[e + 1] * down)));
-        if (lane == 0) q_factor[r] = factor * __uint_as_float(static_cast<uint32_t>(ex) << 23);
+        if (lane == 0) q_factor[r] = kv_row_factor(factor, ex);
       }
     }
     fence_proxy_async_smem();
@@ -374,10 +374,12 @@ struct KvWidePart {
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.s_free[sb]);
       // -- scores
-      if (a.cap > 0.f) {      // cap tanh(t) = cap (1 - 2 / (1 + e^{2 t}))
+      if (a.cap > kKvFineCap) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-          t[j] = a.cap * kKvLog2e * (1.f - 2.f * kv_rcp(1.f + kv_exp2(t[j] * f * (2.f * kKvLog2e)))) - off;
+        for (int j = 0; j < N; ++j) t[j] = kv_cap(t[j] * f, a.cap, true) - off;
+      } else if (a.cap > 0.f) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) t[j] = kv_cap(t[j] * f, a.cap, false) - off;
       } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) t[j] = fmaf(t[j], f, -off);
