@@ -19,14 +19,6 @@ static_assert(kKvTickets + 2 * 4 * kKvPlanSMs * sizeof(uint32_t) <= kKvHeader,
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-int sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return kKvPlanSMs;
-  return n;
-}
-
 bool format_built(int hd, int bits, int group) {
   if (hd != 64 && hd != 128 && hd != 256) return false;
   if (bits != 2 && bits != 4 && bits != 8) return false;
@@ -161,7 +153,7 @@ ttq_status ttq_kv_write(const ttq_kv_cache* cache, const ttq_kv_batch* batch, co
   a.head[0] = k_head, a.head[1] = v_head;
   a.D[0] = cache->D_k, a.D[1] = cache->D_v;
   return status_of(launch_kv_write(a, cache->head_dim, cache->bits, cache->group,
-                                   cache->scheme == TTQ_QSCHEME_SYMMETRIC, dtype, sms(),
+                                   cache->scheme == TTQ_QSCHEME_SYMMETRIC, dtype, device_sms(),
                                    static_cast<cudaStream_t>(stream)));
 }
 
@@ -174,7 +166,7 @@ ttq_status ttq_kv_read(const ttq_kv_cache* cache, const ttq_kv_batch* batch, voi
   if (batch->rows == 0 || batch->batch == 0 || (K == nullptr && V == nullptr)) return TTQ_OK;
   a.y[0] = K, a.y[1] = V;
   a.Dr[0] = cache->D_k_rsqrt, a.Dr[1] = cache->D_v_rsqrt;
-  return status_of(launch_kv_read(a, cache->head_dim, cache->bits, cache->group, dtype, sms(),
+  return status_of(launch_kv_read(a, cache->head_dim, cache->bits, cache->group, dtype, device_sms(),
                                   static_cast<cudaStream_t>(stream)));
 }
 

@@ -12,7 +12,7 @@
 // the grid, so that contexts of any lengths load the SMs evenly.  The warps
 // of a block share out its part of a segment, keep softmax states of their
 // own and merge them at its end.  Of a segment that several runs share each
-// leaves a partial result (running maximum, sum and accumulator) in the
+// leaves a partial result (offset, sum and accumulator) in the
 // workspace, and the one whose ticket is the segment's last merges them in
 // their order, so that the result does not depend on who is last; where
 // there are many, groups of them are merged before the whole.
@@ -184,14 +184,6 @@ __device__ __forceinline__ void kv_lds(uint32_t addr, uint32_t* v) {
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
 
-// A lane's words of one half of a part.
-template <int LB, int PIECE>
-__device__ __forceinline__ void kv_lane_words(uint32_t part, int lane, int half, uint32_t* v) {
-#pragma unroll
-  for (int c = 0; c < LB / PIECE; ++c)
-    kv_lds<PIECE / 4>(part + (c * 2 + half) * 32 * PIECE + lane * PIECE, v + c * (PIECE / 4));
-}
-
 // The offset pairs of a word: p[i] holds the i-th field of the low and of
 // the high half, plus 64 (even fields) or 64 / 16 (odd fields of INT4 / INT2).
 template <int BITS>
@@ -322,7 +314,7 @@ __device__ __forceinline__ uint32_t kv_visible(const KvAttentionArgs& a, int row
 
 namespace ttq {
 
-// A block's shape: NT tiles of 8 rows a warp's products, or (NT = 16) the 128 rows of kv_attention_wide.cuh.
+// A block's shape: NT tiles of 8 rows a warp's products, or (NT = 16) the 256 rows of kv_attention_wide.cuh.
 template <int HD, int BITS, int NG, int NT>
 struct KvShape {
   using A = KvAttention<HD, BITS, NG, NT>;

@@ -105,9 +105,9 @@ struct KvAttentionArgs {
   float* part = nullptr;        // two partial results per block of the grid
   uint32_t* tickets = nullptr;  // two per block of the grid, zero before and after
 };
-// How a launch is laid out: 8 nt query rows per tile, `grid` blocks of
-// kKvAttentionWarps warps, the floats of one partial result, and the bytes
-// of the workspace's regions.
+// How a launch is laid out: 8 nt query rows per tile in blocks of
+// kKvAttentionWarps warps, or (nt = 16) 256 rows in blocks of 16 warps; `grid`
+// blocks; the floats of one partial result, and the bytes of all.
 constexpr int kKvAttentionWarps = 4;
 struct KvAttentionPlan {
   int nt, grid;

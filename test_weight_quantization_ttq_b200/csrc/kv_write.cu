@@ -16,10 +16,10 @@ __device__ __forceinline__ KvGroup group_of(float mn, float mx, uint32_t& flags)
   constexpr int QMAX = (1 << BITS) - 1;
   KvGroup k;
   // the range; of the symmetric schemes the largest magnitude (mn is 0)
-  const float range = __fsub_rn(mx, mn), span = range;
+  const float range = __fsub_rn(mx, mn);
   float s32;
-  if constexpr (BITS == 8) s32 = div_by_const<448>(span);
-  else s32 = div_by_const<SYM ? (1 << (BITS - 1)) - 1 : QMAX>(span);
+  if constexpr (BITS == 8) s32 = div_by_const<448>(range);
+  else s32 = div_by_const<SYM ? (1 << (BITS - 1)) - 1 : QMAX>(range);
   if (!(s32 >= 6.103515625e-05f)) s32 = 6.103515625e-05f;   // 2^-14
   const __half s16 = __float2half_ru(s32);
   const float s = __half2float(s16);

@@ -28,6 +28,8 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+}  // namespace
+
 int device_sms() {
   static std::atomic<int> cache[64] = {};   // host threads that race here store the same value
   int dev = 0;
@@ -42,6 +44,8 @@ int device_sms() {
   if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
+
+namespace {
 
 bool valid_qparams(int bits, int group) {
   return ((bits >= 2 && bits <= 4) || bits == 8) &&

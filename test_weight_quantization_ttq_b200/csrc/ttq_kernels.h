@@ -30,6 +30,9 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// SMs of the current device (148 where it cannot be asked), asked once a device.
+int device_sms();
+
 // Number of token splits of the statistic pass and the rows each covers.
 void act_norm_plan(int64_t d, int64_t T, int num_sms, int64_t* splits, int64_t* rows_per_split);
 
