@@ -143,8 +143,10 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
  * each with the kv_len that ends at its last row.
  *   The products run on the tensor cores with binary16 operands and fp32
  * accumulation: each row of Q (times D_k_rsqrt), scaled by a power of two,
- * is rounded to binary16 (bf16 and binary16 rows lose nothing to it but
- * elements under 2^-14 of the row's largest), the codes less their zeros
+ * is rounded to binary16 (bf16 and binary16 rows without D_k_rsqrt lose
+ * nothing to it but elements under 2^-14 of the row's largest) or, where it
+ * is float32 or times D_k_rsqrt and Y is not bf16, to the sum of two binary16
+ * (22 bits; the products with K are done twice), the codes less their zeros
  * are exact, the probabilities times V's scales are rounded to binary16, in
  * units in which the largest product of a probability and a scale that the
  * row meets is near 1: products under 2^-14 of it are subnormal and keep

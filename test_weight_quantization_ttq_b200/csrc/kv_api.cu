@@ -103,18 +103,20 @@ constexpr int64_t kWideBlocks = 8192;
 // heads up to 128 in one or two groups, where each stands for 6 tiles of 32
 // or more: trees of 24 with 192 rows 76 us (6 tiles 83), trees of 64 with
 // 256 rows 138 (8 tiles 165); one of fewer rows costs as much, so that 5
-// would be about even.
-KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows, int64_t blocks) {
+// would be about even.  Q in two parts has no tiles of 24 and 256 rows (its
+// second set of fragments does not fit beside the operands of 256).
+KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows, int64_t blocks, int q_parts) {
   KvAttentionPlan p = {};
   if (!format_built(hd, bits, group)) return p;
   const int64_t tiles32 = (tile_rows + 31) / 32, tiles256 = (tile_rows + 255) / 256;
-  if (hd <= 128 && hd / group <= 2 && tiles256 > 0 && tiles32 >= 6 * tiles256 && blocks >= kWideBlocks) p.nt = 16;
+  if (hd <= 128 && hd / group <= 2 && q_parts == 1 && tiles256 > 0 && tiles32 >= 6 * tiles256 && blocks >= kWideBlocks) p.nt = 16;
   else if (tile_rows <= 8) p.nt = 1;
   else if (tile_rows <= 16 || hd == 256) p.nt = 2;
-  else p.nt = (tile_rows + 23) / 24 == tiles32 ? 3 : 4;
-  const int ctas = hd == 64    ? kv_attention_ctas_hd64(bits, group, p.nt)
-                   : hd == 128 ? kv_attention_ctas_hd128(bits, group, p.nt)
-                               : kv_attention_ctas_hd256(bits, group, p.nt);
+  else p.nt = q_parts == 1 && (tile_rows + 23) / 24 == tiles32 ? 3 : 4;
+  p.q_parts = q_parts;
+  const int ctas = hd == 64    ? kv_attention_ctas_hd64(bits, group, p.nt, q_parts)
+                   : hd == 128 ? kv_attention_ctas_hd128(bits, group, p.nt, q_parts)
+                               : kv_attention_ctas_hd256(bits, group, p.nt, q_parts);
   p.grid = ctas * kKvPlanSMs;
   p.slot_floats = static_cast<int64_t>(p.nt == 16 ? 256 : 8 * p.nt) * (hd + 4);
   p.part_bytes = static_cast<int64_t>(p.grid) * 2 * p.slot_floats * 4;
@@ -179,7 +181,7 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
   const int64_t tile_rows = max_new * (heads / kv_heads);
   int64_t most = 0;
   for (const int64_t rows : {8, 16, 24, 32, 256}) {
-    const KvAttentionPlan p = kv_attention_plan(head_dim, bits, group, tile_rows < rows ? tile_rows : rows, INT64_MAX);
+    const KvAttentionPlan p = kv_attention_plan(head_dim, bits, group, tile_rows < rows ? tile_rows : rows, INT64_MAX, 1);
     if (p.grid == 0) return 0;
     if (p.part_bytes > most) most = p.part_bytes;
   }
@@ -206,7 +208,16 @@ ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch
   const int per = static_cast<int>(heads / cache->kv_heads);
   const int64_t longest = batch->table_stride * a.g.page_blocks;   // blocks that a sequence may have (below 2^44)
   const int64_t blocks = batch->batch * cache->kv_heads * (longest < (1 << 27) ? longest : 1 << 27);
-  const KvAttentionPlan p = kv_attention_plan(cache->head_dim, cache->bits, cache->group, batch->max_new * per, blocks);
+  // Q times D_k^{-1/2}, and float32 rows, do not fit binary16: an element is then
+  // taken as two of them, so that scores are as exact as their fp32 sums, but for
+  // outputs in bf16, whose own rounding is 8 times the one that a single binary16 costs.
+  // (One alone put binary16 outputs 1.5 to 2.2 times as far off as their rounding
+  // does.  The price, with D and outputs in binary16 against bf16: 64 sequences of up
+  // to 8192 115 us against 90, window and cap 37 and 30, chains of 5 43 and 40, trees of
+  // 24, in tiles of 32 rows then, 128 and 75.)
+  const int q_parts = y_dtype != TTQ_BF16 && (dtype == TTQ_F32 || cache->D_k_rsqrt != nullptr) ? 2 : 1;
+  const KvAttentionPlan p = kv_attention_plan(cache->head_dim, cache->bits, cache->group, batch->max_new * per, blocks,
+                                              q_parts);
   a.Dk = cache->D_k_rsqrt;
   a.Dv = cache->D_v_rsqrt;
   a.Q = Q;

@@ -41,7 +41,7 @@
 // the B operand's by an 8 x 8 transposition within the warp.
 //
 // Numerics.  Each row of q (times D_k^{-1/2}) is scaled by a power of two to
-// [1, 2) and rounded to binary16.  Scores t (in powers of two), the row's
+// [1, 2) and rounded to binary16, or to a sum of two (QP).  Scores t (in powers of two), the row's
 // offset and the sum l are fp32.  What is rounded to binary16 is p s_V, so the
 // offset that p = 2^(t - offset) is taken off by is not the largest score but
 // the largest t + e of the tokens that the row sees, 2^e the power of two in
@@ -70,15 +70,20 @@ __device__ __forceinline__ float kv_exponent(float x) {
   return __uint_as_float(__float_as_uint(x) >> 23 | 0x4B000000u) - 8388735.f;   // 2^23 + 127
 }
 
-template <int HD, int BITS, int NG, int NT>
+// QP: the binary16 numbers that an element of Q is taken as, 1 or 2 (kv_api.cu
+// says when).  Two are two sets of fragments, whose products add to the same
+// scores.
+template <int HD, int BITS, int NG, int NT, int QP>
 struct KvAttention {
   using F = KvFormat<HD, BITS, NG>;
   static constexpr int W = kKvAttentionWarps;       // warps of a block
   static constexpr int ROWS = 8 * NT;               // query rows of a tile
   static constexpr int KS = HD / 16;                // k steps of the first product
   static constexpr int MT = HD / 16;                // m tiles of the second
-  static constexpr int QFRAG = NT * KS * 32 * 8;    // the tile's Q fragments
-  static constexpr int ROWINFO = ROWS * (16 + 8 * NG);   // and what is known of its rows
+  static constexpr int FRAGS = NT * KS * 32 * 8;    // fragments of one part of the tile's Q
+  static constexpr int QPART = FRAGS + ROWS * 8 * NG;   // with the sums of its groups
+  static constexpr int QFRAG = QP * QPART;
+  static constexpr int ROWINFO = ROWS * 16;         // what is known of the rows
   static constexpr int LDO = HD + 4;                // padded row of the accumulators in shared memory
   static constexpr int TILE = ROWS * LDO * 4;       // their bytes
   // whether V's codes are taken raw and their zeros off the sums (see above)
@@ -315,19 +320,19 @@ __device__ __forceinline__ uint32_t kv_visible(const KvAttentionArgs& a, int row
 namespace ttq {
 
 // A block's shape: NT tiles of 8 rows a warp's products, or (NT = 16) the 256 rows of kv_attention_wide.cuh.
-template <int HD, int BITS, int NG, int NT>
+template <int HD, int BITS, int NG, int NT, int QP>
 struct KvShape {
-  using A = KvAttention<HD, BITS, NG, NT>;
+  using A = KvAttention<HD, BITS, NG, NT, QP>;
 };
 template <int HD, int BITS, int NG>
-struct KvShape<HD, BITS, NG, 16> {
+struct KvShape<HD, BITS, NG, 16, 1> {
   using A = KvWide<HD, BITS, NG>;
 };
 
-template <int HD, int BITS, int NG, int NT>
-__global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<HD, BITS, NG, NT>::A::CTAS)
+template <int HD, int BITS, int NG, int NT, int QP>
+__global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT, QP>::A::W * 32, KvShape<HD, BITS, NG, NT, QP>::A::CTAS)
     kv_attention_kernel(const KvAttentionArgs a) {
-  using A = typename KvShape<HD, BITS, NG, NT>::A;
+  using A = typename KvShape<HD, BITS, NG, NT, QP>::A;
   using F = typename A::F;
   constexpr bool WIDE = NT == 16;
   constexpr int W = A::W, ROWS = A::ROWS, OV = A::OVERHEAD;
@@ -522,8 +527,9 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
     const int gr = lane >> 2, tq = lane & 3;    // row group and quarter of the MMA fragments
     uint8_t* ring = smem + warp * A::WARP_BYTES;
     uint32_t* qfrag = reinterpret_cast<uint32_t*>(smem + W * A::WARP_BYTES);
-    float* q_sum = reinterpret_cast<float*>(row_pos + ROWS);       // [NG][ROWS] sums of a row's group
-    float* q_off = q_sum + NG * ROWS;                              // the same with the fields' offsets as weights
+    // behind a part's fragments: [NG][ROWS] sums of a row's group, and the same with the fields' offsets as weights
+    float* q_sum = reinterpret_cast<float*>(smem + W * A::WARP_BYTES + A::FRAGS);
+    float* q_off = q_sum + NG * ROWS;
     uint64_t* bars = all_bars + warp * STAGES;
     int* absent = all_absent + warp * STAGES;
     // of these this warp's: [blk0, blk0 + count)
@@ -620,8 +626,13 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
           const int c = lane * E + e, kg = c / F::G, j = c % F::G;
           const int quarter = j / (F::G / 4), idx = kg * (F::G / 4) + j % (F::G / 4);
           // two k steps of a lane stand side by side
-          qfrag[(((r >> 3) * (KS / 2) + idx / 8) * 32 + 4 * (r & 7) + quarter) * 4 + (idx % 8) / 2] =
-              h2_as_u32(__floats2half2_rn(v[e] * down, v[e + 1] * down));
+          uint32_t* at = qfrag + (((r >> 3) * (KS / 2) + idx / 8) * 32 + 4 * (r & 7) + quarter) * 4 + (idx % 8) / 2;
+          const __half2 q = __floats2half2_rn(v[e] * down, v[e + 1] * down);
+          *at = h2_as_u32(q);
+          if constexpr (QP == 2) {              // what that rounding left (exact in fp32)
+            const float2 f = __half22float2(q);
+            at[A::QPART / 4] = h2_as_u32(__floats2half2_rn(fmaf(v[e], down, -f.x), fmaf(v[e + 1], down, -f.y)));
+          }
         }
         if (lane == 0) q_factor[r] = kv_row_factor(factor, ex);
       }
@@ -631,20 +642,20 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
       // the sums of each group of the rounded rows: the first product with
       // ones, and (INT2, whose fields' offsets differ) with the offsets, as codes
 #pragma unroll 1
-      for (int kn = warp; kn < NG * NT; kn += W) {
-        const int k = kn / NT, nt = kn % NT;
+      for (int kn = warp; kn < QP * NG * NT; kn += W) {
+        const int k = kn / NT % NG, nt = kn % NT, part = kn / (NG * NT) * (A::QPART / 4);
         float one[4] = {}, off[4] = {};
 #pragma unroll
         for (int j = 0; j < KS / NG; ++j) {
           const int ks = k * (KS / NG) + j;
-          const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + ((nt * (KS / 2) + ks / 2) * 32 + lane) * 4 + ks % 2 * 2);
+          const uint2 bq = *reinterpret_cast<const uint2*>(qfrag + part + ((nt * (KS / 2) + ks / 2) * 32 + lane) * 4 + ks % 2 * 2);
           kv_mma(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, bq.x, bq.y);
           if constexpr (BITS == 2) kv_mma(off, A::EVEN, A::EVEN, A::ODD, A::ODD, bq.x, bq.y);
         }
         if (gr == 0) {
-          *reinterpret_cast<float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq) = make_float2(one[0], one[1]);
+          *reinterpret_cast<float2*>(q_sum + part + k * ROWS + 8 * nt + 2 * tq) = make_float2(one[0], one[1]);
           if constexpr (BITS == 2)
-            *reinterpret_cast<float2*>(q_off + k * ROWS + 8 * nt + 2 * tq) = make_float2(off[0], off[1]);
+            *reinterpret_cast<float2*>(q_off + part + k * ROWS + 8 * nt + 2 * tq) = make_float2(off[0], off[1]);
         }
       }
       __syncthreads();
@@ -685,62 +696,69 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT>::A::W * 32, KvShape<
       const bool masked = gone || done < plain0 || done >= plain1;
       // -- scores
       float s[NT][4];
+      if constexpr (QP == 2) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      }
       uint32_t kp[2][NG];
       kv_lds<NG>(st + F::CODES + gr * NG * 4, kp[0]);
       kv_lds<NG>(st + F::CODES + (gr + 8) * NG * 4, kp[1]);
       constexpr int KSG = KS / NG;              // k steps of a group
       constexpr int KSW = BITS == 8 ? 1 : 32 / BITS / 4;   // k steps of a word
       uint32_t kw[2][PW], pa[2][2 * KSW];
+#pragma unroll 1
+      for (int part = 0; part < A::QFRAG; part += A::QPART) {   // of Q: its offset
 #pragma unroll
-      for (int k = 0; k < NG; ++k) {
-        float acc[NT][4];
-        uint32_t bq[NT][4];                     // Q's fragments of two k steps
+        for (int k = 0; k < NG; ++k) {
+          float acc[NT][4];
+          uint32_t bq[NT][4];                     // Q's fragments of two k steps
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+          for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 #pragma unroll
-        for (int j = 0; j < KSG; ++j) {
-          const int ks = k * KSG + j, w = ks / KSW, in = ks % KSW;
+          for (int j = 0; j < KSG; ++j) {
+            const int ks = k * KSG + j, w = ks / KSW, in = ks % KSW;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            if (in == 0 && w % PW == 0)
-              kv_lds<PW>(st + (w / PW * 2 + r) * 32 * F::PIECE + lane * F::PIECE, kw[r]);
-            if (in == 0) {
-              if constexpr (BITS == 8) kv_e4m3x4(kw[r][w % PW], pa[r][0], pa[r][1]);
-              else kv_offset_pairs<BITS>(kw[r][w % PW], magic, pa[r]);
+            for (int r = 0; r < 2; ++r) {
+              if (in == 0 && w % PW == 0)
+                kv_lds<PW>(st + (w / PW * 2 + r) * 32 * F::PIECE + lane * F::PIECE, kw[r]);
+              if (in == 0) {
+                if constexpr (BITS == 8) kv_e4m3x4(kw[r][w % PW], pa[r][0], pa[r][1]);
+                else kv_offset_pairs<BITS>(kw[r][w % PW], magic, pa[r]);
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (ks % 2 == 0) kv_lds<4>(q_frags + part + (nt * (KS / 2) + ks / 2) * 512, bq[nt]);
+              kv_mma(acc[nt], pa[0][2 * in], pa[1][2 * in], pa[0][2 * in + 1], pa[1][2 * in + 1], bq[nt][ks % 2 * 2],
+                     bq[nt][ks % 2 * 2 + 1]);
             }
           }
+          const float2 p0 = __half22float2(u32_as_h2(kp[0][k])), p1 = __half22float2(u32_as_h2(kp[1][k]));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if (ks % 2 == 0) kv_lds<4>(q_frags + (nt * (KS / 2) + ks / 2) * 512, bq[nt]);
-            kv_mma(acc[nt], pa[0][2 * in], pa[1][2 * in], pa[0][2 * in + 1], pa[1][2 * in + 1], bq[nt][ks % 2 * 2],
-                   bq[nt][ks % 2 * 2 + 1]);
-          }
-        }
-        const float2 p0 = __half22float2(u32_as_h2(kp[0][k])), p1 = __half22float2(u32_as_h2(kp[1][k]));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (BITS != 8) {
-            const float2 qs = *reinterpret_cast<const float2*>(q_sum + k * ROWS + 8 * nt + 2 * tq);
-            float z0 = p0.y, z1 = p1.y;
-            if constexpr (BITS == 4) {          // both fields are offset by 64
-              z0 += 64.f, z1 += 64.f;
-            } else {
-              const float2 qo = *reinterpret_cast<const float2*>(q_off + k * ROWS + 8 * nt + 2 * tq);
-              acc[nt][0] -= qo.x, acc[nt][1] -= qo.y, acc[nt][2] -= qo.x, acc[nt][3] -= qo.y;
+            if constexpr (BITS != 8) {
+              const float2 qs = *reinterpret_cast<const float2*>(q_sum + part / 4 + k * ROWS + 8 * nt + 2 * tq);
+              float z0 = p0.y, z1 = p1.y;
+              if constexpr (BITS == 4) {          // both fields are offset by 64
+                z0 += 64.f, z1 += 64.f;
+              } else {
+                const float2 qo = *reinterpret_cast<const float2*>(q_off + part / 4 + k * ROWS + 8 * nt + 2 * tq);
+                acc[nt][0] -= qo.x, acc[nt][1] -= qo.y, acc[nt][2] -= qo.x, acc[nt][3] -= qo.y;
+              }
+              acc[nt][0] = fmaf(-z0, qs.x, acc[nt][0]);
+              acc[nt][1] = fmaf(-z0, qs.y, acc[nt][1]);
+              acc[nt][2] = fmaf(-z1, qs.x, acc[nt][2]);
+              acc[nt][3] = fmaf(-z1, qs.y, acc[nt][3]);
             }
-            acc[nt][0] = fmaf(-z0, qs.x, acc[nt][0]);
-            acc[nt][1] = fmaf(-z0, qs.y, acc[nt][1]);
-            acc[nt][2] = fmaf(-z1, qs.x, acc[nt][2]);
-            acc[nt][3] = fmaf(-z1, qs.y, acc[nt][3]);
-          }
-          if (k == 0) {
-            s[nt][0] = acc[nt][0] * p0.x, s[nt][1] = acc[nt][1] * p0.x;
-            s[nt][2] = acc[nt][2] * p1.x, s[nt][3] = acc[nt][3] * p1.x;
-          } else {
-            s[nt][0] = fmaf(acc[nt][0], p0.x, s[nt][0]);
-            s[nt][1] = fmaf(acc[nt][1], p0.x, s[nt][1]);
-            s[nt][2] = fmaf(acc[nt][2], p1.x, s[nt][2]);
-            s[nt][3] = fmaf(acc[nt][3], p1.x, s[nt][3]);
+            if (QP == 1 && k == 0) {
+              s[nt][0] = acc[nt][0] * p0.x, s[nt][1] = acc[nt][1] * p0.x;
+              s[nt][2] = acc[nt][2] * p1.x, s[nt][3] = acc[nt][3] * p1.x;
+            } else {
+              s[nt][0] = fmaf(acc[nt][0], p0.x, s[nt][0]);
+              s[nt][1] = fmaf(acc[nt][1], p0.x, s[nt][1]);
+              s[nt][2] = fmaf(acc[nt][2], p1.x, s[nt][2]);
+              s[nt][3] = fmaf(acc[nt][3], p1.x, s[nt][3]);
+            }
           }
         }
       }
@@ -1121,22 +1139,25 @@ cudaError_t kv_attention_hd64(const KvAttentionArgs& a, int bits, int group, con
 cudaError_t kv_attention_hd128(const KvAttentionArgs& a, int bits, int group, const KvAttentionPlan& p, cudaStream_t s);
 cudaError_t kv_attention_hd256(const KvAttentionArgs& a, int bits, int group, const KvAttentionPlan& p, cudaStream_t s);
 // Blocks per SM of the same kernels; 0 if the format is not built.
-int kv_attention_ctas_hd64(int bits, int group, int nt);
-int kv_attention_ctas_hd128(int bits, int group, int nt);
-int kv_attention_ctas_hd256(int bits, int group, int nt);
+int kv_attention_ctas_hd64(int bits, int group, int nt, int q_parts);
+int kv_attention_ctas_hd128(int bits, int group, int nt, int q_parts);
+int kv_attention_ctas_hd256(int bits, int group, int nt, int q_parts);
 
-// Calls f(BITS, NG, NT) as constants for one head size; false if not built.
+// Calls f(BITS, NG, NT, QP) as constants for one head size; false if not built.
 template <int HD, typename Fn>
-bool kv_with_format(int bits, int group, int nt, Fn&& f) {
+bool kv_with_format(int bits, int group, int nt, int q_parts, Fn&& f) {
   auto tiles = [&](auto BITSc, auto NGc) {
-    if (nt == 1) return f(BITSc, NGc, std::integral_constant<int, 1>{}), true;
-    if (nt == 2) return f(BITSc, NGc, std::integral_constant<int, 2>{}), true;
-    if constexpr (HD <= 128 && decltype(NGc)::value <= 2)
-      if (nt == 16) return f(BITSc, NGc, std::integral_constant<int, 16>{}), true;
+    constexpr std::integral_constant<int, 1> one{};
+    constexpr std::integral_constant<int, 2> two{};
+    if (nt == 1) return q_parts == 1 ? f(BITSc, NGc, one, one) : f(BITSc, NGc, one, two), true;
+    if (nt == 2) return q_parts == 1 ? f(BITSc, NGc, two, one) : f(BITSc, NGc, two, two), true;
     if constexpr (HD <= 128) {
-      if (nt == 3) return f(BITSc, NGc, std::integral_constant<int, 3>{}), true;
-      if (nt == 4) return f(BITSc, NGc, std::integral_constant<int, 4>{}), true;
+      constexpr std::integral_constant<int, 4> four{};
+      if (nt == 4) return q_parts == 1 ? f(BITSc, NGc, four, one) : f(BITSc, NGc, four, two), true;
+      if (nt == 3 && q_parts == 1) return f(BITSc, NGc, std::integral_constant<int, 3>{}, one), true;
     }
+    if constexpr (HD <= 128 && decltype(NGc)::value <= 2)
+      if (nt == 16 && q_parts == 1) return f(BITSc, NGc, std::integral_constant<int, 16>{}, one), true;
     return false;
   };
   auto groups = [&](auto BITSc) {
@@ -1154,10 +1175,10 @@ bool kv_with_format(int bits, int group, int nt, Fn&& f) {
 }
 
 template <int HD>
-int kv_attention_ctas(int bits, int group, int nt) {
+int kv_attention_ctas(int bits, int group, int nt, int q_parts) {
   int n = 0;
-  kv_with_format<HD>(bits, group, nt, [&](auto B, auto G, auto N) {
-    n = KvShape<HD, decltype(B)::value, decltype(G)::value, decltype(N)::value>::A::CTAS;
+  kv_with_format<HD>(bits, group, nt, q_parts, [&](auto B, auto G, auto N, auto P) {
+    n = KvShape<HD, decltype(B)::value, decltype(G)::value, decltype(N)::value, decltype(P)::value>::A::CTAS;
   });
   return n;
 }
@@ -1166,10 +1187,10 @@ template <int HD>
 cudaError_t kv_attention_launch(const KvAttentionArgs& a, int bits, int group, const KvAttentionPlan& p,
                                 cudaStream_t stream) {
   cudaError_t e = cudaErrorInvalidValue;
-  kv_with_format<HD>(bits, group, p.nt, [&](auto Bc, auto Gc, auto Nc) {
-    constexpr int BITS = decltype(Bc)::value, NG = decltype(Gc)::value, NT = decltype(Nc)::value;
-    using A = typename KvShape<HD, BITS, NG, NT>::A;
-    auto* kernel = kv_attention_kernel<HD, BITS, NG, NT>;
+  kv_with_format<HD>(bits, group, p.nt, p.q_parts, [&](auto Bc, auto Gc, auto Nc, auto Pc) {
+    constexpr int BITS = decltype(Bc)::value, NG = decltype(Gc)::value, NT = decltype(Nc)::value, QP = decltype(Pc)::value;
+    using A = typename KvShape<HD, BITS, NG, NT, QP>::A;
+    auto* kernel = kv_attention_kernel<HD, BITS, NG, NT, QP>;
     const int smem = A::SMEM + 16 * a.g.batch;
     static std::atomic<uint64_t> set{0};
     if ((e = kv_allow_smem(reinterpret_cast<const void*>(kernel), A::SMEM + 16 * kKvMaxBatch, set)) != cudaSuccess) return;

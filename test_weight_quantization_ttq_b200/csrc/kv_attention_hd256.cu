@@ -7,6 +7,8 @@ cudaError_t kv_attention_hd256(const KvAttentionArgs& a, int bits, int group, co
                               cudaStream_t stream) {
   return kv_attention_launch<256>(a, bits, group, p, stream);
 }
-int kv_attention_ctas_hd256(int bits, int group, int nt) { return kv_attention_ctas<256>(bits, group, nt); }
+int kv_attention_ctas_hd256(int bits, int group, int nt, int q_parts) {
+  return kv_attention_ctas<256>(bits, group, nt, q_parts);
+}
 
 }  // namespace ttq

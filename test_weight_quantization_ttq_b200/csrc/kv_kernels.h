@@ -107,15 +107,16 @@ struct KvAttentionArgs {
 };
 // How a launch is laid out: 8 nt query rows per tile in blocks of
 // kKvAttentionWarps warps, or (nt = 16) 256 rows in blocks of 16 warps; `grid`
-// blocks; the floats of one partial result, and the bytes of all.
+// blocks; q_parts binary16 numbers (1 or 2) that an element of Q is taken as;
+// the floats of one partial result, and the bytes of all.
 constexpr int kKvAttentionWarps = 4;
 struct KvAttentionPlan {
-  int nt, grid;
+  int nt, grid, q_parts;
   int64_t slot_floats, part_bytes;
 };
 // blocks: as many as the batch's sequences may have, of all heads.  grid 0: the
 // format is not built.
-KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows, int64_t blocks);
+KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows, int64_t blocks, int q_parts);
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, int hd, int bits, int group,
                                 const KvAttentionPlan& plan, cudaStream_t stream);
 
