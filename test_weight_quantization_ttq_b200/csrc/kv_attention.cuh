@@ -781,18 +781,17 @@ __global__ void __launch_bounds__(KvShape<HD, BITS, NG, NT, QP>::A::W * 32, KvSh
         }
       }
       // -- scores in powers of two less the row's offset
+      auto scaled = [&](auto of) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float2 f = *reinterpret_cast<const float2*>(q_factor + 8 * nt + 2 * tq);
-        if (a.cap > 0.f) {
-          const bool fine = a.cap > kKvFineCap;
+        for (int nt = 0; nt < NT; ++nt) {
+          const float2 f = *reinterpret_cast<const float2*>(q_factor + 8 * nt + 2 * tq);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] = kv_cap(s[nt][i] * ((i & 1) ? f.y : f.x), a.cap, fine) - off[nt][i & 1];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] = fmaf(s[nt][i], (i & 1) ? f.y : f.x, -off[nt][i & 1]);
+          for (int i = 0; i < 4; ++i) s[nt][i] = of(s[nt][i], (i & 1) ? f.y : f.x, off[nt][i & 1]);
         }
-      }
+      };
+      if (!(a.cap > 0.f)) scaled([](float x, float f, float o) { return fmaf(x, f, -o); });
+      else if (a.cap > kKvFineCap) scaled([&](float x, float f, float o) { return kv_cap(x * f, a.cap, true) - o; });
+      else scaled([&](float x, float f, float o) { return kv_cap(x * f, a.cap, false) - o; });
       // -- masks: lane r finds which of the block's tokens row r sees; tokens
       // that are not there count for nothing, whatever their bytes are
       if (masked) {
