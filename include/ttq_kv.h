@@ -55,7 +55,8 @@
  *    more than max_new or kv_len, or with kv_len beyond its table, is
  *    skipped, and a position whose page is not in [0, num_pages) is skipped (written
  *    nowhere, read as absent: zeros from ttq_kv_read, not attended to);
- *    both set TTQ_FLAG_BAD_INDEX.
+ *    both set TTQ_FLAG_BAD_INDEX.  Of a sequence without rows nothing else is
+ *    looked at, and it sets no flag.
  */
 #ifndef TTQ_KV_H_
 #define TTQ_KV_H_
@@ -140,7 +141,13 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
  *     ones that it sees besides itself (its depth in the tree).
  * The new tokens' own K and V are read from the cache: write them first.
  * max_new is at most 64: a longer piece of a prompt goes in pieces of 64,
- * each with the kv_len that ends at its last row.
+ * each with the kv_len that ends at its last row.  With max_new 0 nothing is
+ * done or checked on the device.
+ *   heads, max_new and the room that the page table has (batch x table_stride
+ * pages) choose how many query rows a thread block takes together, for all
+ * sequences alike: a table wider than the contexts need, or one sequence with
+ * many rows beside many with one, costs time (give the latter a call of their
+ * own), and results of another choice differ in their last bits.
  *   The products run on the tensor cores with binary16 operands and fp32
  * accumulation: each row of Q (times D_k_rsqrt), scaled by a power of two,
  * is rounded to binary16 (bf16 and binary16 rows without D_k_rsqrt lose
@@ -155,9 +162,9 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
  * products.)  What a row does not see has no effect on it.  Scores, their
  * running maxima and sums are fp32; a capped score is off by 2^-22 of the cap
  * where that is at most 256, else by 2^-19 of itself, and a cap of 2^64 or
- * more, which changes no fp32 score, is left out.  Deterministic for given inputs.  ws:
- * ttq_kv_attention_workspace_size(...) bytes, initialised once by
- * ttq_workspace_init (every call leaves its counters at zero) and again
+ * more, which changes no fp32 score, is left out.  Deterministic for given
+ * inputs.  ws: ttq_kv_attention_workspace_size(...) bytes, initialised once
+ * by ttq_workspace_init (every call leaves its counters at zero) and again
  * after TIMEOUT; calls that may run at the same time need one each.  Flags
  * BAD_INDEX and TIMEOUT. */
 ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch, const void* Q,

@@ -87,8 +87,11 @@ constexpr float kKvMostCap = 18446744073709551616.f, kKvLeastCap = 1.f / kKvMost
 
 // Tiles of 256 rows pay where there is work for them: the blocks that the
 // batch's sequences may have, by the width of its page table (32 heads over 8,
-// trees of 48: 4000 blocks 54 us, 42 in tiles of 32; 8000 blocks 69 and 66;
-// trees of 64: 4000 blocks 60 and 50, 16448 blocks 138 and 165).
+// trees of 48: 4000 blocks 55 us, 42 in tiles of 32; 8000 blocks 71 and 68;
+// trees of 64: 4000 blocks 61 and 51, 16448 blocks of E4M3 with a cap 135 and 170).
+// The lengths themselves are on the device: a table much wider than they need
+// takes these tiles where those of 32 were faster (a table 8 times as wide: trees
+// of 24 over 8 contexts of 500 43 us against 37, of 64 over 2 of 2000 50 against 35).
 constexpr int64_t kWideBlocks = 8192;
 
 // 8, 16, 24 or 32 query rows per tile: the fewest that hold a sequence's rows
@@ -101,8 +104,8 @@ constexpr int64_t kWideBlocks = 8192;
 // 165.)  Heads of 256 channels stop at 16 (their accumulators fill the
 // registers).  The tiles of 256 rows of kv_attention_wide.cuh (nt = 16), of
 // heads up to 128 in one or two groups, where each stands for 6 tiles of 32
-// or more: trees of 24 with 192 rows 76 us (6 tiles 83), trees of 64 with
-// 256 rows 138 (8 tiles 165); one of fewer rows costs as much, so that 5
+// or more: trees of 24 with 192 rows 75 us (6 tiles 84), trees of 64 with
+// 256 rows 134 (8 tiles 170); one of fewer rows costs as much, so that 5
 // would be about even.  Q in two parts has no tiles of 24 and 256 rows (its
 // second set of fragments does not fit beside the operands of 256).
 KvAttentionPlan kv_attention_plan(int hd, int bits, int group, int64_t tile_rows, int64_t blocks, int q_parts) {

@@ -18,7 +18,7 @@
 // there are many, groups of them are merged before the whole.
 // (One run per warp, with no barrier between warps, was measured too: it
 // left every cut to a single warp's merge, 6 us at 2 to 9 results, and took
-// 97 us where this takes 88 for 64 contexts of up to 8192.)
+// 97 us where this takes 87 for 64 contexts of up to 8192.)
 //
 // A warp brings its blocks through a ring of shared memory stages by bulk
 // copies, one per block (codes and pairs of K and V are contiguous).

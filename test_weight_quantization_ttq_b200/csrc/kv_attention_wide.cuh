@@ -22,11 +22,14 @@
 // The operands are in two buffers, and S too where tensor memory holds it
 // (one group), so that the next step's scores and unpacking overlap this
 // one's softmax.
-// Measured: trees of 64 over 16384 positions of E4M3, cap, 256 rows: 138 us
-// (8 tiles of 32: 165); trees of 24, 192 rows: 76 us (83).  Bound by the
-// latency of the softmax's steps, not by a pipe (the tensor pipe is 11% busy):
-// two threads a row (138 and 80 us), tiles of 128 rows (136 and 92) and warps
-// that sleep while they wait (143 and 100) were not better.
+// Measured: trees of 64 over 16384 positions of E4M3, cap, 256 rows: 134 us
+// (8 tiles of 32: 170); trees of 24, 192 rows: 75 us (84).  Bound by the
+// latency of the softmax's steps, not by a pipe (tensor pipe 13 to 14% busy,
+// instructions issued in 40 to 46% of the cycles; the longest wait, a third, is
+// for loads from tensor and global memory).  Both 128-row halves move in step,
+// through the same barriers.  When these two took 138 and 76 us, two threads a row (138 and 80),
+// tiles of 128 rows (136 and 92) and warps that sleep while they wait (143 and
+// 100) were not better.
 #pragma once
 
 #include "kv_device.cuh"

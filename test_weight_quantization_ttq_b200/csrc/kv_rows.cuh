@@ -16,7 +16,7 @@
 // all lanes contiguous, a group's range is found by 2 (K) or 3 (V) shuffles,
 // and a row's place is looked up once per 16 rows.  (A thread per 8 channels
 // of one row, with its own search, took 84 and 70 us where these take 47 and
-// 36: the prompts of 5 requests, 12020 rows of 8 heads, written as INT4 codes
+// 35: the prompts of 5 requests, 12020 rows of 8 heads, written as INT4 codes
 // and read back, and 32785 positions read.)
 // Rows of the dense tensors are read 16 bytes a lane; they are written
 // through shared memory, so that a store covers whole rows.
