@@ -179,15 +179,18 @@ size_t ttq_kv_attention_workspace_size(int head_dim, int bits, int group, int64_
                                        int64_t kv_heads, int64_t max_new) {
   if (kv_heads < 1 || heads < kv_heads || heads % kv_heads != 0 || heads > 65535) return 0;
   if (max_new < 0 || max_new > kKvMaxNew) return 0;
-  // the most of what any context lengths and any fewer rows take: the plans of
-  // every width of tile up to the rows' own
+  // the most of what any types, context lengths and fewer rows take: the plans
+  // of every width of tile up to the rows' own, for Q in one part and in two
+  // (which has other tiles)
   const int64_t tile_rows = max_new * (heads / kv_heads);
   int64_t most = 0;
-  for (const int64_t rows : {8, 16, 24, 32, 256}) {
-    const KvAttentionPlan p = kv_attention_plan(head_dim, bits, group, tile_rows < rows ? tile_rows : rows, INT64_MAX, 1);
-    if (p.grid == 0) return 0;
-    if (p.part_bytes > most) most = p.part_bytes;
-  }
+  for (const int q_parts : {1, 2})
+    for (const int64_t rows : {8, 16, 24, 32, 256}) {
+      const int64_t tile = tile_rows < rows ? tile_rows : rows;
+      const KvAttentionPlan p = kv_attention_plan(head_dim, bits, group, tile, INT64_MAX, q_parts);
+      if (p.grid == 0) return 0;
+      if (p.part_bytes > most) most = p.part_bytes;
+    }
   return kKvHeader + most;
 }
 
@@ -221,6 +224,7 @@ ttq_status ttq_kv_attention(const ttq_kv_cache* cache, const ttq_kv_batch* batch
   const int q_parts = y_dtype != TTQ_BF16 && (dtype == TTQ_F32 || cache->D_k_rsqrt != nullptr) ? 2 : 1;
   const KvAttentionPlan p = kv_attention_plan(cache->head_dim, cache->bits, cache->group, batch->max_new * per, blocks,
                                               q_parts);
+  if (ws_bytes < kKvHeader + static_cast<size_t>(p.part_bytes)) return TTQ_ERR_WORKSPACE;   // (need is the most of all plans)
   a.Dk = cache->D_k_rsqrt;
   a.Dv = cache->D_v_rsqrt;
   a.Q = Q;
