@@ -41,15 +41,15 @@
 // the B operand's by an 8 x 8 transposition within the warp.
 //
 // Numerics.  Each row of q (times D_k^{-1/2}) is scaled by a power of two to
-// [1, 2) and rounded to binary16, or to a sum of two (QP).  Scores t (in powers of two), the row's
-// offset and the sum l are fp32.  What is rounded to binary16 is p s_V, so the
-// offset that p = 2^(t - offset) is taken off by is not the largest score but
-// the largest t + e of the tokens that the row sees, 2^e the power of two in
-// the token's largest scale of V (its groups share it): p s_V of the weightiest
-// token is near 1, whatever the scales are, and a token that the row does not
-// see, or that has no probability, takes no bits from the others.  The offset
-// moves only when a t + e exceeds it by more than 8, which keeps p s_V below
-// 2^9; products under 2^-14 are binary16's subnormal numbers.
+// [1, 2) and rounded to binary16, or to a sum of two (QP).  Scores t (in
+// powers of two), the row's offset and the sum l are fp32.  What is rounded to
+// binary16 is p s_V, so the offset in p = 2^(t - offset) is not the largest
+// score but the largest t + e of the tokens that the row sees, 2^e the power of
+// two in the token's largest scale of V (its groups share it): p s_V of the
+// weightiest token is near 1, whatever the scales are, and a token that the row
+// does not see, or that has no probability, takes no bits from the others.
+// The offset moves only when a t + e exceeds it by more than 8, which keeps
+// p s_V below 2^9; products under 2^-14 are binary16's subnormal numbers.
 #pragma once
 
 #include <atomic>

@@ -27,9 +27,9 @@
 // latency of the softmax's steps, not by a pipe (tensor pipe 13 to 14% busy,
 // instructions issued in 40 to 46% of the cycles; the longest wait, a third, is
 // for loads from tensor and global memory).  Both 128-row halves move in step,
-// through the same barriers.  When these two took 138 and 76 us, two threads a row (138 and 80),
-// tiles of 128 rows (136 and 92) and warps that sleep while they wait (143 and
-// 100) were not better.
+// through the same barriers.  When these two took 138 and 76 us, two threads a
+// row (138 and 80), tiles of 128 rows (136 and 92) and warps that sleep while
+// they wait (143 and 100) were not better.
 #pragma once
 
 #include "kv_device.cuh"
